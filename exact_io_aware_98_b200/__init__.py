@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -24,6 +24,7 @@ _STATUS = {0: "FA_OK", -1: "FA_ERR_INVALID", -2: "FA_ERR_UNSUPPORTED", -3: "FA_E
 
 # exported symbol -> (restype, argtypes)
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_l = ctypes.c_int64
 SIGNATURES = {
     "fa_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp, _i, _vp]),
     "fa_fwd_gqa": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _vp, _i, _vp]),
@@ -38,6 +39,14 @@ SIGNATURES = {
                             _vp, _vp, _i, _vp]),
     "fa_bwd_deterministic_ex": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
                                      _i, _f, _i, _vp, _vp, _i, _vp, _sz, _i, _vp]),
+    "fa_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _l, _f, _i, _i, _vp]),
+    "fa_paged_plan": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _l, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
+                           _vp, _vp]),
+    "fa_paged_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp,
+                             _l, _l, _i, _i, _f, _i, _i, _vp]),
+    "fa_paged_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_paged_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _l, _l, _l,
+                          _l, _l, _i, _i, _i, _i, _f, _i, _i, _vp, _sz, _vp]),
     "fa_fwd_tile_reference": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp,
                                    _i, _i, _vp]),
     "fa_naive_workspace_size": (_sz, [_i, _i, _i]),
@@ -249,6 +258,290 @@ def bwd_noalloc(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool
                             _dtype_code(q), _stream())
     _check(rc, "fa_bwd_noalloc")
     return dq, dk, dv
+
+
+# ----------------------------------------------------------------- rotary positions, paged cache
+ROPE_INTERLEAVED, ROPE_BACKWARD = 1, 2   # fa.h FA_ROPE_*
+
+
+def _on(device, t, name: str, dtype=None):
+    """Checks that t is on ``device`` (a CUDA device) with ``dtype``; no contiguity asked."""
+    if not t.is_cuda:
+        raise FaError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise FaError(f"{name} is on {t.device}, not {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise FaError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _flat(device, t, name: str, dtype, shape=None):
+    """_on for a contiguous tensor, of ``shape`` when given."""
+    _on(device, t, name, dtype)
+    if not t.is_contiguous():
+        raise FaError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise FaError(f"{name} shape {tuple(t.shape)} must be {tuple(shape)}")
+
+
+def _call(device, name: str, *args):
+    """One library call on ``device``'s current stream, whatever device is current."""
+    fn = getattr(load(), name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != 0:
+        _check(rc, name)
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+                     factor: float = 1.0, original_length: Optional[int] = None,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq, magnitude) for ``rope`` and ``paged_append``: float64 [rotary_dim / 2] radians
+    per position on ``device``, base^(-2i / rotary_dim), scaled for contexts ``factor`` times
+    longer:
+      None        unscaled
+      "linear"    every frequency divided by ``factor``
+      "ntk"       base times factor^(rotary_dim / (rotary_dim - 2)): the lowest frequency is
+                  divided by ``factor``, the highest stays
+      "by_parts"  (YaRN, arXiv 2309.00071) frequencies that turn at least ``beta_fast`` times in
+                  ``original_length`` positions stay, those that turn at most ``beta_slow`` times
+                  are divided by ``factor``, linearly between; magnitude 0.1 ln(factor) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise FaError(f"rotary_dim must be even and positive, got {rotary_dim}")
+    if not (base > 0.0 and math.isfinite(base)) or not (factor >= 1.0 and math.isfinite(factor)):
+        raise FaError("base must be positive, factor at least 1, both finite")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2.0))
+    f = base ** (-2.0 * i / rotary_dim)
+    magnitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "by_parts":
+        if original_length is None or original_length < 1 or not beta_fast > beta_slow:
+            raise FaError('"by_parts" needs original_length >= 1 and beta_fast > beta_slow')
+        keep = ((original_length * f / (2.0 * math.pi) - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+        magnitude = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise FaError(f"unknown scaling {scaling!r}")
+    return f.to(device), magnitude
+
+
+def _rope(x, inv_freq, positions, interleaved, magnitude, out, backward):
+    dev = x.device
+    _on(dev, x, "x")
+    _flat(dev, inv_freq, "inv_freq", torch.float64)
+    packed = x.dim() == 3
+    if not packed and x.dim() != 4:
+        raise FaError(f"x must be [B, H, N, d] or [T, H, d], got {tuple(x.shape)}")
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+    if out is not None:
+        _on(dev, y, "out", x.dtype)
+        if y.shape != x.shape:
+            raise FaError(f"out shape {tuple(y.shape)} must be {tuple(x.shape)}")
+    d = x.shape[-1]
+    if d > 1 and (x.stride(-1) != 1 or y.stride(-1) != 1):
+        raise FaError("the last dimension of x and out must be contiguous")
+    xs, ys = x.stride(), y.stride()
+    if packed:
+        (N, H), B = x.shape[:2], 1
+        xs, ys = (0, xs[1], xs[0]), (0, ys[1], ys[0])
+    else:
+        B, H, N = x.shape[:3]
+    ps = 0
+    if positions is not None:
+        _on(dev, positions, "positions", torch.int32)
+        if positions.shape != (N,) and (packed or positions.shape != (B, N)):
+            raise FaError(f"positions shape {tuple(positions.shape)} does not match x {tuple(x.shape)}")
+        if N > 1 and positions.stride(-1) != 1:
+            raise FaError("positions must be contiguous along the tokens")
+        ps = positions.stride(0) if positions.dim() == 2 else 0
+    _call(dev, "fa_rope", x.data_ptr(), y.data_ptr(), _ptr(positions), inv_freq.data_ptr(), B, H, N,
+          d, 2 * inv_freq.numel(), (_l * 3)(*xs[:3]), (_l * 3)(*ys[:3]), ps, float(magnitude),
+          (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_BACKWARD if backward else 0),
+          _dtype_code(x))
+    return y
+
+
+def rope(x, inv_freq, positions=None, interleaved: bool = False, magnitude: float = 1.0, out=None):
+    """Rotary positions (fa_rope) on x [B, H, N, d] or packed [T, H, d], bf16 or fp32, any
+    strides with d contiguous; the first 2 * len(inv_freq) columns turn.  positions int32 [N]
+    or [B, N] ([T] when packed), default 0 .. N-1.  ``out`` may be x."""
+    return _rope(x, inv_freq, positions, interleaved, magnitude, out, False)
+
+
+def rope_bwd(dy, inv_freq, positions=None, interleaved: bool = False, magnitude: float = 1.0,
+             out=None):
+    """dL/dx of ``rope`` from dL/dy, with the same arguments."""
+    return _rope(dy, inv_freq, positions, interleaved, magnitude, out, True)
+
+
+class PagedPlan(NamedTuple):
+    """Outputs of ``paged_plan`` (int32, slots int64)."""
+    cu_q: torch.Tensor       # [B + 1] first row of each request's new tokens
+    kv_len: torch.Tensor     # [B] cached keys including the new tokens
+    positions: torch.Tensor  # [max_tokens]
+    slots: torch.Tensor      # [max_tokens], -1: not stored
+    counts: torch.Tensor     # [4] tokens asked for, pages taken, pages short, cursor after
+
+    @classmethod
+    def empty(cls, B: int, max_tokens: int, device="cuda"):
+        i32 = lambda n: torch.empty(n, dtype=torch.int32, device=device)
+        return cls(i32(B + 1), i32(B), i32(max_tokens),
+                   torch.empty(max_tokens, dtype=torch.int64, device=device), i32(4))
+
+
+def paged_plan(ctx_len, new_len, free_pages, block_table, page_size: int, max_tokens: int,
+               cursor=None, out: Optional[PagedPlan] = None) -> PagedPlan:
+    """One step's bookkeeping on the GPU (fa_paged_plan): ctx_len and new_len int32 [B],
+    free_pages int32 [F] (handed out from ``cursor``, int32 [1], on), block_table int32
+    [B, max_pages] updated in place.  ``out`` reuses an earlier plan's tensors."""
+    dev = ctx_len.device
+    B = ctx_len.numel()
+    _flat(dev, ctx_len, "ctx_len", torch.int32, (B,))
+    _flat(dev, new_len, "new_len", torch.int32, (B,))
+    _flat(dev, free_pages, "free_pages", torch.int32)
+    _on(dev, block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise FaError(f"block_table must be [{B}, max_pages] with contiguous rows")
+    if cursor is not None:
+        _flat(dev, cursor, "cursor", torch.int32)
+        if cursor.numel() != 1:
+            raise FaError("cursor must hold one number")
+    max_tokens = int(max_tokens)
+    if out is None:
+        if max_tokens < 1 or B < 1:
+            raise FaError("paged_plan needs at least one request and max_tokens >= 1")
+        out = PagedPlan.empty(B, max_tokens, dev)
+    else:
+        for t, n, dt, size in ((out.cu_q, "cu_q", torch.int32, B + 1), (out.kv_len, "kv_len", torch.int32, B),
+                               (out.positions, "positions", torch.int32, max_tokens),
+                               (out.slots, "slots", torch.int64, max_tokens),
+                               (out.counts, "counts", torch.int32, 4)):
+            _flat(dev, t, n, dt, (size,))
+    _call(dev, "fa_paged_plan", ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
+          free_pages.numel(), _ptr(cursor), block_table.data_ptr(), block_table.stride(0), B,
+          block_table.shape[1], int(page_size), max_tokens, out.cu_q.data_ptr(),
+          out.kv_len.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
+          out.counts.data_ptr())
+    return out
+
+
+def _cache(dev, k_cache, v_cache, dtype, H_kv: int, d: int):
+    """Checks of a paged cache pair [num_pages, H_kv, page_size, d]; (num_pages, page_size)."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _on(dev, t, n, dtype)
+        if t.dim() != 4 or t.shape[1] != H_kv or t.shape[3] != d or t.shape != k_cache.shape:
+            raise FaError(f"{n} shape {tuple(t.shape)} must be [pages, {H_kv}, page_size, {d}]")
+        page = t.shape[2]
+        if t.stride(3) != 1 or t.stride(2) != d or (H_kv > 1 and t.stride(1) != page * d):
+            raise FaError(f"each page of {n} must be contiguous")
+    return k_cache.shape[0], k_cache.shape[2]
+
+
+def paged_append(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None,
+                 interleaved: bool = False, magnitude: float = 1.0, q=None, q_out=None):
+    """Stores k and v [T, H_kv, d] at their slots (int64 [T]) of the caches [pages, H_kv,
+    page_size, d] (fa_paged_append); with inv_freq and positions (int32 [T]) the keys are rotated
+    as ``rope`` does.  q [T, H, d] is rotated alongside into q_out (allocated when None; may be
+    q), which is returned (None without q)."""
+    dev = k.device
+    _on(dev, k, "k")
+    _on(dev, v, "v", k.dtype)
+    if k.dim() != 3 or v.shape != k.shape:
+        raise FaError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must both be [T, H_kv, d]")
+    T, H_kv, d = k.shape
+    pages, page = _cache(dev, k_cache, v_cache, k.dtype, H_kv, d)
+    _flat(dev, slots, "slots", torch.int64, (T,))
+    rot = 0
+    if inv_freq is not None:
+        _flat(dev, inv_freq, "inv_freq", torch.float64)
+        if positions is None:
+            raise FaError("inv_freq needs positions")
+        _flat(dev, positions, "positions", torch.int32, (T,))
+        rot = 2 * inv_freq.numel()
+    H = 0
+    qs = qos = (0, 0, 1)
+    if q is not None:
+        _on(dev, q, "q", k.dtype)
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
+            raise FaError(f"q shape {tuple(q.shape)} must be [{T}, H, {d}]")
+        H = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _on(dev, q_out, "q_out", q.dtype)
+            if q_out.shape != q.shape:
+                raise FaError(f"q_out shape {tuple(q_out.shape)} must be {tuple(q.shape)}")
+        qs, qos = q.stride(), q_out.stride()
+    elif q_out is not None:
+        raise FaError("q_out without q")
+    ks, vs = k.stride(), v.stride()
+    if d > 1 and (qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or qos[2] != 1):
+        raise FaError("the last dimension of q, k, v and q_out must be contiguous")
+    _call(dev, "fa_paged_append", _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out),
+          k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(),
+          None if rot == 0 else positions.data_ptr(), _ptr(inv_freq), T, H, H_kv, d, rot,
+          (_l * 8)(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qos[0], qos[1]), k_cache.stride(0),
+          v_cache.stride(0), page, pages, float(magnitude), ROPE_INTERLEAVED if interleaved else 0,
+          _dtype_code(k))
+    return q_out
+
+
+def paged_workspace_size(T: int, B: int, H: int, H_kv: int, d: int) -> int:
+    return int(load().fa_paged_workspace_size(T, B, H, H_kv, d))
+
+
+def paged_fwd(q, k_cache, v_cache, block_table, kv_len, cu_q, scale: Optional[float] = None,
+              causal: bool = True, max_q: Optional[int] = None, out=None, lse=None, workspace=None):
+    """O, lse of each request's new tokens over its paged cache (fa_paged_fwd): q [T, H, d] (any
+    token and head strides), caches [pages, H_kv, page_size, d], block_table int32
+    [B, max_pages], kv_len int32 [B], cu_q int32 [B + 1].  O is [T, H, d], lse [T, H]; rows that
+    no request owns are not written.  ``max_q``, the most new tokens of any request, helps to
+    choose the kernel."""
+    dev = q.device
+    _on(dev, q, "q")
+    if q.dim() != 3:
+        raise FaError(f"q must be [T, H, d], got {tuple(q.shape)}")
+    T, H, d = q.shape
+    if d > 1 and q.stride(2) != 1:
+        raise FaError("the last dimension of q must be contiguous")
+    if k_cache.dim() != 4:
+        raise FaError("k_cache must be [pages, H_kv, page_size, d]")
+    H_kv = k_cache.shape[1]
+    pages, page = _cache(dev, k_cache, v_cache, q.dtype, H_kv, d)
+    B = kv_len.numel()
+    _flat(dev, kv_len, "kv_len", torch.int32, (B,))
+    _flat(dev, cu_q, "cu_q", torch.int32, (B + 1,))
+    _on(dev, block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise FaError(f"block_table must be [{B}, max_pages] with contiguous rows")
+    if out is None:
+        out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+    else:
+        _flat(dev, out, "out", q.dtype, q.shape)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _flat(dev, lse, "lse", torch.float32, (T, H))
+    if workspace is None:
+        workspace = torch.empty(paged_workspace_size(T, B, H, H_kv, d), dtype=torch.uint8, device=dev)
+    else:
+        _flat(dev, workspace, "workspace", torch.uint8)
+    qs = q.stride()
+    _call(dev, "fa_paged_fwd", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_table.data_ptr(), kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+          T, B, H, H_kv, d, qs[0], qs[1], k_cache.stride(0), v_cache.stride(0),
+          block_table.stride(0), page, pages, block_table.shape[1],
+          0 if max_q is None else int(max_q), default_scale(d) if scale is None else float(scale),
+          int(causal), _dtype_code(q), workspace.data_ptr(), workspace.numel())
+    return out, lse
 
 
 TILE_REVERSE = 1          # fa.h FA_TILE_REVERSE: key tiles visited last to first

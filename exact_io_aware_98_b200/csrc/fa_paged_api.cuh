@@ -1,0 +1,415 @@
+// fa_paged_api.cuh -- host side of the rotary and paged-cache entry points: argument checks,
+// the choice of kernel and launch shape, launches.  Included by fa_api.cu, whose helpers
+// (fail, check_launch, launch_ex, set_smem, tensor-map encoding) it uses.
+#pragma once
+
+namespace {
+
+constexpr int kSms = 148;            // B200; grids and workspaces are sized by it
+constexpr int kMaxPagedCtas = 4 * kSms;
+
+bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int dtype_bytes(int dtype) { return dtype == FA_BF16 ? 2 : (dtype == FA_F32 ? 4 : 0); }
+
+int log2_page(int page_size) {
+  if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return -1;
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+
+// ---- rotary -----------------------------------------------------------------------------
+// Vector width for rows of d columns of which `rot` turn: 16 bytes where every row start and
+// every piece of a row allows it, else one element.
+int rope_vec(int es, int d, int rot, bool rows16) {
+  const int v = 16 / es;
+  return rows16 && (rot / 2) % v == 0 && (d - rot) % v == 0 ? v : 1;
+}
+
+// Tokens and heads per block: about four 16-byte pairs per thread, fewer while the grid would
+// leave SMs without two blocks.
+void rope_tiles(long long N, int H, int B, int units, int half, int* tb, int* hc) {
+  const int want = 4 * fa::ROPE_THREADS;
+  int h = std::max(1, std::min(H, want / std::max(1, units)));
+  int t = std::max(1, want / std::max(1, units * h));
+  if (half > 0) t = std::min(t, fa::ROPE_TABLE / half);
+  t = static_cast<int>(std::min<long long>(t, N));
+  auto blocks = [&]() { return ((N + t - 1) / t) * ((H + h - 1) / h) * B; };
+  while (blocks() < 2 * kSms && static_cast<long long>(t) * h * units > fa::ROPE_THREADS) {
+    if (t > 1) t = (t + 1) / 2;
+    else if (h > 1) h = (h + 1) / 2;
+    else break;
+  }
+  *tb = t;
+  *hc = h;
+}
+
+template <typename T, int V>
+void (*rope_kernel(bool il))(const fa::RopeParams) {
+  return il ? fa::fa_rope_kernel<T, V, true> : fa::fa_rope_kernel<T, V, false>;
+}
+template <typename T, int V>
+void (*append_kernel(bool il))(const fa::AppendParams) {
+  return il ? fa::fa_paged_append_kernel<T, V, true> : fa::fa_paged_append_kernel<T, V, false>;
+}
+
+// ---- paged attention ----------------------------------------------------------------------
+// One kernel variant: rows and keys of a tile and CTAs of the grid.
+struct PagedShape {
+  int rows, ctas;
+};
+
+size_t paged_ws_part(long long T, int group, int d, PagedShape v, int* rows_cap, size_t* off_ml,
+                     size_t* off_o) {
+  const int splits = (group + v.rows - 1) / v.rows;
+  const int G = (group + splits - 1) / splits;
+  const long long cap = std::min<long long>(v.rows, (T * G + 7) / 8 * 8);
+  const size_t head = round256(static_cast<size_t>(v.ctas) * sizeof(int4));
+  const size_t ml = round256(static_cast<size_t>(v.ctas) * 2 * cap * sizeof(float2));
+  if (rows_cap != nullptr) {
+    *rows_cap = static_cast<int>(cap);
+    *off_ml = head;
+    *off_o = head + ml;
+  }
+  return head + ml + round256(static_cast<size_t>(v.ctas) * 2 * cap * d * sizeof(float));
+}
+
+// CTAs of a CUDA-core variant: what shared memory lets an SM hold, up to four.
+PagedShape simt_shape(bool few, int d) {
+  const size_t smem = few ? fa::PagedSimtLayout<1, 4>::bytes(d) : fa::PagedSimtLayout<4, 1>::bytes(d);
+  const int per_sm = static_cast<int>(std::min<size_t>(4, 233472 / (smem + 1024)));
+  return {few ? 8 : 32, kSms * per_sm};
+}
+
+size_t paged_ws_bytes(long long T, int group, int d) {
+  size_t n = 0;
+  for (const PagedShape v : {simt_shape(true, d), simt_shape(false, d)})
+    n = std::max(n, paged_ws_part(T, group, d, v, nullptr, nullptr, nullptr));
+  return n;
+}
+
+template <typename T>
+int launch_join(const fa::PagedParams& p, int ctas, cudaStream_t s) {
+  // blocks per split item: a warp per row
+  const int by = (p.rows_cap + fa::JOIN_WARPS - 1) / fa::JOIN_WARPS;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, std::min(by, 16));
+  cfg.blockDim = dim3(fa::JOIN_WARPS * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::fa_paged_join_kernel<T>, p);
+  if (e != cudaSuccess) return fail(FA_ERR_CUDA, "fa_paged_join_kernel: %s", cudaGetErrorString(e));
+  return check_launch("fa_paged_join_kernel");
+}
+
+// Lays the workspace out for a variant and sets the tile fields of the parameters.
+void paged_tiles(fa::PagedParams& p, PagedShape v, int H_kv, void* ws) {
+  size_t off_ml = 0, off_o = 0;
+  p.splits = (p.group + v.rows - 1) / v.rows;
+  p.G = (p.group + p.splits - 1) / p.splits;
+  p.Hv = H_kv * p.splits;
+  paged_ws_part(p.T, p.group, p.d, v, &p.rows_cap, &off_ml, &off_o);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  p.ws_head = reinterpret_cast<int4*>(b);
+  p.ws_ml = reinterpret_cast<float2*>(b + off_ml);
+  p.ws_o = reinterpret_cast<float*>(b + off_o);
+}
+
+template <typename T, int WR, int WK>
+int launch_paged_simt(fa::PagedParams p, int H_kv, void* ws, cudaStream_t s) {
+  using L = fa::PagedSimtLayout<WR, WK>;
+  const PagedShape v = simt_shape(WK > 1, p.d);
+  paged_tiles(p, v, H_kv, ws);
+  const size_t smem = L::bytes(p.d);
+  int rc = set_smem(fa::fa_paged_simt_kernel<T, WR, WK>, static_cast<int>(smem));
+  if (rc != FA_OK) return rc;
+  fa::fa_paged_simt_kernel<T, WR, WK><<<v.ctas, 128, smem, s>>>(p);
+  if ((rc = check_launch("fa_paged_simt_kernel")) != FA_OK) return rc;
+  return launch_join<T>(p, v.ctas, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_rope(const void* x, void* y, const int32_t* positions, const double* inv_freq, int B, int H,
+            int N, int d, int rotary_dim, const int64_t* x_strides, const int64_t* y_strides,
+            int64_t positions_stride, float magnitude, int options, int dtype, void* stream) {
+  const int es = dtype_bytes(dtype);
+  if (es == 0) return fail(FA_ERR_INVALID, "unknown dtype %d", dtype);
+  if ((options & ~(FA_ROPE_INTERLEAVED | FA_ROPE_BACKWARD)) != 0)
+    return fail(FA_ERR_INVALID, "unknown rotary options 0x%x", options);
+  if (B < 0 || H < 1 || N < 0 || d < 1) return fail(FA_ERR_INVALID, "B, N >= 0 and H, d >= 1 required");
+  if (d > 1024) return fail(FA_ERR_UNSUPPORTED, "d <= 1024 required, got %d", d);
+  if (rotary_dim < 2 || rotary_dim > d || (rotary_dim & 1) != 0)
+    return fail(FA_ERR_INVALID, "rotary_dim must be even and in [2, d], got %d", rotary_dim);
+  if (!std::isfinite(magnitude)) return fail(FA_ERR_INVALID, "magnitude must be finite");
+  if (x_strides == nullptr || y_strides == nullptr) return fail(FA_ERR_INVALID, "null strides");
+  if (B == 0 || N == 0) return FA_OK;
+  if (!x || !y || !inv_freq) return fail(FA_ERR_INVALID, "null tensor pointer");
+  if (N > (1 << 24)) return fail(FA_ERR_UNSUPPORTED, "N too large");
+  const int ext[3] = {B, H, N};
+  bool rows16 = aligned_to(x, 16) && aligned_to(y, 16);
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] < 2) continue;
+    if (y_strides[i] == 0) return fail(FA_ERR_INVALID, "the output's strides must not be 0");
+    if (x == y && x_strides[i] != y_strides[i])
+      return fail(FA_ERR_INVALID, "in place, input and output strides must be equal");
+    rows16 = rows16 && (x_strides[i] * es) % 16 == 0 && (y_strides[i] * es) % 16 == 0;
+  }
+  if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(inv_freq, 8) ||
+      !aligned_to(positions, 4))
+    return fail(FA_ERR_ALIGN, "a pointer is not aligned to its elements");
+  fa::RopeParams p;
+  p.x = x;
+  p.y = y;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  for (int i = 0; i < 3; ++i) {
+    p.xs[i] = x_strides[i];
+    p.ys[i] = y_strides[i];
+  }
+  p.pos_sb = positions_stride;
+  p.B = B;
+  p.H = H;
+  p.N = N;
+  p.rot = rotary_dim;
+  const int V = rope_vec(es, d, rotary_dim, rows16);
+  p.n_rot = rotary_dim / 2 / V;
+  p.n_units = p.n_rot + (x == y ? 0 : (d - rotary_dim) / V);  // in place, the rest stays
+  p.heads_inner = std::llabs(x_strides[1]) < std::llabs(x_strides[2]) ? 1 : 0;
+  rope_tiles(N, H, B, p.n_units, rotary_dim / 2, &p.tb, &p.hc);
+  p.n_hchunks = (H + p.hc - 1) / p.hc;
+  p.mag = magnitude;
+  p.sgn = (options & FA_ROPE_BACKWARD) ? -1.0f : 1.0f;
+  const long long gx = static_cast<long long>((N + p.tb - 1) / p.tb) * p.n_hchunks;
+  if (gx > 0x7fffffffll) return fail(FA_ERR_UNSUPPORTED, "grid too large");
+  const bool il = (options & FA_ROPE_INTERLEAVED) != 0;
+  auto* kern = dtype == FA_BF16 ? (V > 1 ? rope_kernel<__nv_bfloat16, 8>(il) : rope_kernel<__nv_bfloat16, 1>(il))
+                                : (V > 1 ? rope_kernel<float, 4>(il) : rope_kernel<float, 1>(il));
+  kern<<<dim3(static_cast<unsigned>(gx), std::min(B, 65535)), fa::ROPE_THREADS, 0,
+         static_cast<cudaStream_t>(stream)>>>(p);
+  return check_launch("fa_rope_kernel");
+}
+
+int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t* free_pages,
+                  int n_free, const int32_t* cursor, int32_t* block_table, int64_t table_stride,
+                  int B, int max_pages, int page_size, int max_tokens, int32_t* cu_q,
+                  int32_t* kv_len, int32_t* positions, int64_t* slots, int32_t* counts,
+                  void* stream) {
+  const int shift = log2_page(page_size);
+  if (shift < 0) return fail(FA_ERR_INVALID, "page_size must be a power of two in [16, 1024], got %d", page_size);
+  if (B < 1 || max_pages < 1 || max_tokens < 1 || n_free < 0)
+    return fail(FA_ERR_INVALID, "B, max_pages, max_tokens >= 1 and n_free >= 0 required");
+  if (!ctx_len || !new_len || (!free_pages && n_free > 0) || !block_table || !cu_q || !kv_len ||
+      !positions || !slots || !counts)
+    return fail(FA_ERR_INVALID, "null pointer");
+  if (B > 1 && table_stride < max_pages)
+    return fail(FA_ERR_INVALID, "block-table rows overlap: stride %lld for %d pages",
+                static_cast<long long>(table_stride), max_pages);
+  if (!aligned_to(ctx_len, 4) || !aligned_to(new_len, 4) || !aligned_to(free_pages, 4) ||
+      !aligned_to(cursor, 4) || !aligned_to(block_table, 4) || !aligned_to(cu_q, 4) ||
+      !aligned_to(kv_len, 4) || !aligned_to(positions, 4) || !aligned_to(slots, 8) ||
+      !aligned_to(counts, 4))
+    return fail(FA_ERR_ALIGN, "a pointer is not aligned to its elements");
+  fa::PlanParams p;
+  p.ctx_len = ctx_len;
+  p.new_len = new_len;
+  p.free_pages = free_pages;
+  p.cursor = cursor;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.cu_q = cu_q;
+  p.kv_len = kv_len;
+  p.positions = positions;
+  p.counts = counts;
+  p.slots = reinterpret_cast<long long*>(slots);
+  p.B = B;
+  p.n_free = n_free;
+  p.max_pages = max_pages;
+  p.max_tokens = max_tokens;
+  p.page_shift = shift;
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(max_tokens) + fa::PLAN_THREADS - 1) / fa::PLAN_THREADS);
+  fa::fa_paged_plan_kernel<<<grid, fa::PLAN_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return check_launch("fa_paged_plan_kernel");
+}
+
+int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                    void* v_cache, const int64_t* slots, const int32_t* positions,
+                    const double* inv_freq, int T, int H, int H_kv, int d, int rotary_dim,
+                    const int64_t* strides, int64_t k_page_stride, int64_t v_page_stride,
+                    int page_size, int num_pages, float magnitude, int options, int dtype,
+                    void* stream) {
+  const int es = dtype_bytes(dtype);
+  if (es == 0) return fail(FA_ERR_INVALID, "unknown dtype %d", dtype);
+  if ((options & ~FA_ROPE_INTERLEAVED) != 0) return fail(FA_ERR_INVALID, "unknown append options 0x%x", options);
+  const int shift = log2_page(page_size);
+  if (shift < 0) return fail(FA_ERR_INVALID, "page_size must be a power of two in [16, 1024], got %d", page_size);
+  if (T < 0 || H < 0 || H_kv < 1 || d < 1 || num_pages < 1)
+    return fail(FA_ERR_INVALID, "T, H >= 0 and H_kv, d, num_pages >= 1 required");
+  if (d > 1024) return fail(FA_ERR_UNSUPPORTED, "d <= 1024 required, got %d", d);
+  if (strides == nullptr) return fail(FA_ERR_INVALID, "null strides");
+  if (inv_freq == nullptr ? rotary_dim != 0
+                          : (rotary_dim < 2 || rotary_dim > d || (rotary_dim & 1) != 0))
+    return fail(FA_ERR_INVALID, "rotary_dim must be even and in [2, d], or 0 without inv_freq; got %d", rotary_dim);
+  if (inv_freq != nullptr && positions == nullptr && T > 0)
+    return fail(FA_ERR_INVALID, "a rotation needs positions");
+  if (!std::isfinite(magnitude)) return fail(FA_ERR_INVALID, "magnitude must be finite");
+  const long long page_elems = static_cast<long long>(H_kv) * page_size * d;
+  if (num_pages > 1 && (k_page_stride < page_elems || v_page_stride < page_elems))
+    return fail(FA_ERR_INVALID, "cache pages overlap");
+  if (T == 0) return FA_OK;
+  if (!k || !v || !k_cache || !v_cache || !slots || (H > 0 && (!q || !q_out)))
+    return fail(FA_ERR_INVALID, "null tensor pointer");
+  if (T > (1 << 24)) return fail(FA_ERR_UNSUPPORTED, "T too large");
+  // strides: token and head of q, k, v, q_out
+  bool rows16 = aligned_to(k, 16) && aligned_to(v, 16) && aligned_to(k_cache, 16) && aligned_to(v_cache, 16) &&
+                (static_cast<long long>(d) * es) % 16 == 0 && (k_page_stride * es) % 16 == 0 &&
+                (v_page_stride * es) % 16 == 0;
+  bool elems = aligned_to(k, es) && aligned_to(v, es) && aligned_to(k_cache, es) && aligned_to(v_cache, es) &&
+               aligned_to(slots, 8) && aligned_to(positions, 4) && aligned_to(inv_freq, 8);
+  if (H > 0) {
+    rows16 = rows16 && aligned_to(q, 16) && aligned_to(q_out, 16);
+    elems = elems && aligned_to(q, es) && aligned_to(q_out, es);
+  }
+  const int heads[4] = {H, H_kv, H_kv, H};
+  for (int i = H > 0 ? 0 : 1; i < (H > 0 ? 4 : 3); ++i) {
+    if (T > 1) rows16 = rows16 && (strides[2 * i] * es) % 16 == 0;
+    if (heads[i] > 1) rows16 = rows16 && (strides[2 * i + 1] * es) % 16 == 0;
+  }
+  if (H > 0 && ((T > 1 && strides[6] == 0) || (H > 1 && strides[7] == 0)))
+    return fail(FA_ERR_INVALID, "the output's strides must not be 0");
+  if (H > 0 && q == q_out && ((T > 1 && strides[0] != strides[6]) || (H > 1 && strides[1] != strides[7])))
+    return fail(FA_ERR_INVALID, "in place, input and output strides must be equal");
+  if (!elems) return fail(FA_ERR_ALIGN, "a pointer is not aligned to its elements");
+  fa::AppendParams p;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.slots = reinterpret_cast<const long long*>(slots);
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  for (int i = 0; i < 2; ++i) {
+    p.qs[i] = strides[i];
+    p.ks[i] = strides[2 + i];
+    p.vs[i] = strides[4 + i];
+    p.qos[i] = strides[6 + i];
+  }
+  p.k_page = k_page_stride;
+  p.v_page = v_page_stride;
+  p.n_slots = static_cast<long long>(num_pages) << shift;
+  p.T = T;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.d = d;
+  p.rot = rotary_dim;
+  const int V = rope_vec(es, d, rotary_dim, rows16);
+  p.n_rot = rotary_dim / 2 / V;
+  p.n_units = p.n_rot + (d - rotary_dim) / V;
+  p.page_shift = shift;
+  p.mag = magnitude;
+  const int rows = H + 2 * H_kv;
+  rope_tiles(T, rows, 1, p.n_units, rotary_dim / 2, &p.tb, &p.hc);
+  p.n_hchunks = (rows + p.hc - 1) / p.hc;
+  const long long gx = static_cast<long long>((T + p.tb - 1) / p.tb) * p.n_hchunks;
+  if (gx > 0x7fffffffll) return fail(FA_ERR_UNSUPPORTED, "grid too large");
+  const bool il = (options & FA_ROPE_INTERLEAVED) != 0;
+  auto* kern = dtype == FA_BF16 ? (V > 1 ? append_kernel<__nv_bfloat16, 8>(il) : append_kernel<__nv_bfloat16, 1>(il))
+                                : (V > 1 ? append_kernel<float, 4>(il) : append_kernel<float, 1>(il));
+  kern<<<static_cast<unsigned>(gx), fa::ROPE_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return check_launch("fa_paged_append_kernel");
+}
+
+size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d) {
+  if (T < 1 || B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || d < 1 || d > 128) return 0;
+  return paged_ws_bytes(T, H / H_kv, d);
+}
+
+int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
+                 const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_q, void* o,
+                 float* lse, int T, int B, int H, int H_kv, int d, int64_t q_token_stride,
+                 int64_t q_head_stride, int64_t k_page_stride, int64_t v_page_stride,
+                 int64_t table_stride, int page_size, int num_pages, int max_pages, int max_q,
+                 float scale, int causal, int dtype, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  if (T < 0 || B < 1 || H < 1 || d < 1 || num_pages < 1 || max_pages < 1)
+    return fail(FA_ERR_INVALID, "T >= 0 and B, H, d, num_pages, max_pages >= 1 required");
+  int rc = check_groups(H, H_kv);
+  if (rc != FA_OK) return rc;
+  if (!(std::isfinite(scale) && scale > 0.f)) return fail(FA_ERR_INVALID, "scale must be finite and > 0");
+  const int es = dtype_bytes(dtype);
+  if (es == 0) return fail(FA_ERR_INVALID, "unknown dtype %d", dtype);
+  if (dtype == FA_BF16 && d != 64 && d != 128)
+    return fail(FA_ERR_UNSUPPORTED, "bf16 paged attention supports d in {64, 128}, got %d", d);
+  if (d > 128) return fail(FA_ERR_UNSUPPORTED, "paged attention supports d <= 128, got %d", d);
+  const int shift = log2_page(page_size);
+  if (shift < 0) return fail(FA_ERR_INVALID, "page_size must be a power of two in [16, 1024], got %d", page_size);
+  if (T > (1 << 24) || B > (1 << 24)) return fail(FA_ERR_UNSUPPORTED, "T or B too large");
+  if ((static_cast<long long>(max_pages) << shift) > (1ll << 30))
+    return fail(FA_ERR_UNSUPPORTED, "more than 2^30 positions per request");
+  if (static_cast<long long>(H_kv) * num_pages > 0x7fffffffll || (static_cast<long long>(H_kv) << shift) > 0x7fffffffll)
+    return fail(FA_ERR_UNSUPPORTED, "cache too large");
+  if (B > 1 && table_stride < max_pages) return fail(FA_ERR_INVALID, "block-table rows overlap");
+  const long long page_elems = static_cast<long long>(H_kv) * page_size * d;
+  if (num_pages > 1 && (k_page_stride < page_elems || v_page_stride < page_elems))
+    return fail(FA_ERR_INVALID, "cache pages overlap");
+  if (T == 0) return FA_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !kv_len || !cu_q || !o || !lse)
+    return fail(FA_ERR_INVALID, "null tensor pointer");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(lse))
+    return fail(FA_ERR_ALIGN, "tensor pointers must be 16-byte aligned");
+  if (!aligned_to(block_table, 4) || !aligned_to(kv_len, 4) || !aligned_to(cu_q, 4))
+    return fail(FA_ERR_ALIGN, "a pointer is not aligned to its elements");
+  if (dtype == FA_BF16 &&
+      ((T > 1 && q_token_stride % 8 != 0) || (H > 1 && q_head_stride % 8 != 0) ||
+       (num_pages > 1 && (k_page_stride % 8 != 0 || v_page_stride % 8 != 0))))
+    return fail(FA_ERR_ALIGN, "bf16 strides must be multiples of 8 elements");
+  const size_t need = paged_ws_bytes(T, H / H_kv, d);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(FA_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
+  if (!aligned_to(workspace, 256)) return fail(FA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  fa::PagedParams p;
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.o = o;
+  p.lse = lse;
+  p.table = block_table;
+  p.kv_len = kv_len;
+  p.cu_q = cu_q;
+  p.table_stride = table_stride;
+  p.q_st = q_token_stride;
+  p.q_sh = q_head_stride;
+  p.k_page = k_page_stride;
+  p.v_page = v_page_stride;
+  p.T = T;
+  p.B = B;
+  p.H = H;
+  p.group = H / H_kv;
+  p.d = d;
+  p.vec = d % 4 == 0 && (num_pages == 1 || ((k_page_stride * es) % 16 == 0 && (v_page_stride * es) % 16 == 0));
+  p.page_shift = shift;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.causal = causal ? 1 : 0;
+  p.scale2 = scale * kLog2e;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // new tokens per request: the caller's bound, or the batch's mean
+  const long long rows = static_cast<long long>(max_q > 0 ? std::min(max_q, T) : (T + B - 1) / B) * p.group;
+  const bool few = rows <= 8;
+  if (dtype == FA_F32)
+    return few ? launch_paged_simt<float, 1, 4>(p, H_kv, workspace, s)
+               : launch_paged_simt<float, 4, 1>(p, H_kv, workspace, s);
+  return few ? launch_paged_simt<__nv_bfloat16, 1, 4>(p, H_kv, workspace, s)
+             : launch_paged_simt<__nv_bfloat16, 4, 1>(p, H_kv, workspace, s);
+}
+
+}  // extern "C"

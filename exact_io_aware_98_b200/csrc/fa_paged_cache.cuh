@@ -1,0 +1,233 @@
+// fa_paged_cache.cuh -- the paged key/value cache around the attention: the plan of a batch
+// (token offsets, positions, cache slots, block-table entries from the requests' lengths) and
+// the append of new keys and values at those slots, with the rotary rotation of keys and
+// queries.
+//
+// Cache layout: [page][H_kv][page_size][d]; token position p of a request lies in page
+// block_table[request][p / page_size], row p % page_size, and its slot is the number
+// page * page_size + row.
+#pragma once
+#include <cstdint>
+
+#include "fa_rope.cuh"
+
+namespace fa {
+
+// ---------------------------------------------------------------------------------- block scan
+// Exclusive prefix sum over the block's threads; *total gets the sum.  `tmp` is 33 entries of
+// shared memory; every thread of the block calls it (two barriers).
+template <typename T, int NT>
+__device__ __forceinline__ T block_excl_scan(T v, T* tmp, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  T s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T up = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += up;
+  }
+  if (lane == 31) tmp[warp] = s;
+  __syncthreads();
+  T before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const T x = tmp[w];
+    if (w < warp) before += x;
+    all += x;
+  }
+  __syncthreads();  // tmp may be written again
+  *total = all;
+  return before + s - v;
+}
+
+// ---------------------------------------------------------------------------------- plan
+struct PlanParams {
+  const int32_t *ctx_len, *new_len, *free_pages, *cursor;
+  int32_t* table;
+  long long table_stride;
+  int32_t *cu_q, *kv_len, *positions, *counts;
+  long long* slots;
+  int B, n_free, max_pages, max_tokens, page_shift;
+};
+
+constexpr int PLAN_THREADS = 256;
+
+// Each block owns PLAN_THREADS tokens and scans the requests' lengths by itself, PLAN_THREADS
+// requests at a time, until it has passed its tokens: no second launch and no order between
+// blocks.  Bound by the latency of one launch, of the lengths' load, of a page id's load and of
+// the stores; the scan of B requests costs B / 256 further steps.  A page is opened by exactly
+// one token (the one at its first row), and that token's thread writes the table entry; block 0
+// also writes the per-request outputs.
+__global__ void __launch_bounds__(PLAN_THREADS) fa_paged_plan_kernel(const PlanParams p) {
+  __shared__ long long tmp[33];
+  __shared__ int s_start[PLAN_THREADS + 1];  // first token of each request (clamped)
+  __shared__ int s_ctx[PLAN_THREADS];
+  __shared__ int s_base[PLAN_THREADS];       // its first new page's place in the free list
+  const int tid = threadIdx.x;
+  const int t0 = static_cast<int>(blockIdx.x) * PLAN_THREADS;
+  const int tok = t0 + tid;
+  const int t_end = min(t0 + PLAN_THREADS, p.max_tokens);
+  const int page = 1 << p.page_shift;
+  const bool lead = blockIdx.x == 0;
+  const long long cursor = p.cursor == nullptr ? 0 : max(0, *p.cursor);
+  long long asked = 0, pages = 0;  // sums over the requests before this round's
+  for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
+    const int b = b0 + tid;
+    const long long ctx = b < p.B ? max(0, p.ctx_len[b]) : 0;
+    const long long want = b < p.B ? max(0, p.new_len[b]) : 0;
+    long long sum;
+    const long long start = asked + block_excl_scan<long long, PLAN_THREADS>(want, tmp, &sum);
+    // tokens beyond max_tokens are not part of the step
+    const long long got = min(want, max(0ll, p.max_tokens - start));
+    const long long first = (ctx + page - 1) >> p.page_shift;
+    const long long last = min((ctx + got + page - 1) >> p.page_shift,
+                               static_cast<long long>(p.max_pages));
+    long long psum;
+    const long long base =
+        pages + block_excl_scan<long long, PLAN_THREADS>(max(0ll, last - first), tmp, &psum);
+    if (lead && b < p.B) {
+      p.cu_q[b] = static_cast<int>(min(start, static_cast<long long>(p.max_tokens)));
+      p.kv_len[b] = static_cast<int>(min(ctx + got, 0x7fffffffll));
+    }
+    const long long here = min(asked, static_cast<long long>(p.max_tokens));
+    const long long next = min(asked + sum, static_cast<long long>(p.max_tokens));
+    if (here < t_end && next > t0) {
+      s_start[tid] = static_cast<int>(min(start, static_cast<long long>(p.max_tokens)));
+      s_ctx[tid] = static_cast<int>(ctx);
+      s_base[tid] = static_cast<int>(min(base, 0x7fffffffll));
+      __syncthreads();
+      if (tok >= here && tok < next) {
+        // the last request of this round that starts at or before the token (empty requests
+        // share their start with the one that follows, which is later)
+        int lo = 0, hi = min(PLAN_THREADS, p.B - b0);
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_start[mid] <= tok) lo = mid; else hi = mid;
+        }
+        const long long pos = static_cast<long long>(s_ctx[lo]) + (tok - s_start[lo]);
+        const long long at = pos >> p.page_shift;
+        const long long opened = (static_cast<long long>(s_ctx[lo]) + page - 1) >> p.page_shift;
+        int id = -1;
+        if (at < p.max_pages) {
+          int32_t* entry = p.table + (b0 + lo) * p.table_stride + at;
+          if (at >= opened) {
+            const long long k = cursor + s_base[lo] + (at - opened);
+            if (k < p.n_free) id = p.free_pages[k];
+            if ((pos & (page - 1)) == 0) *entry = id;
+          } else {
+            id = *entry;
+          }
+        }
+        p.positions[tok] = static_cast<int>(min(pos, 0x7fffffffll));
+        p.slots[tok] = id < 0 ? -1ll
+                              : (static_cast<long long>(id) << p.page_shift) + (pos & (page - 1));
+      }
+      __syncthreads();  // the shared arrays are rewritten in the next round
+    }
+    asked += sum;
+    pages += psum;
+    if (!lead && asked >= t_end) return;
+  }
+  // padding behind the last request
+  if (tok < p.max_tokens && tok >= asked) {
+    p.positions[tok] = 0;
+    p.slots[tok] = -1;
+  }
+  if (lead && tid == 0) {
+    const long long avail = max(0ll, p.n_free - cursor);
+    const long long taken = min(pages, avail);
+    p.cu_q[p.B] = static_cast<int>(min(asked, static_cast<long long>(p.max_tokens)));
+    p.counts[0] = static_cast<int>(min(asked, 0x7fffffffll));
+    p.counts[1] = static_cast<int>(taken);
+    p.counts[2] = static_cast<int>(min(pages - taken, 0x7fffffffll));
+    p.counts[3] = static_cast<int>(min(cursor + taken, 0x7fffffffll));
+  }
+}
+
+// ---------------------------------------------------------------------------------- append
+struct AppendParams {
+  const void *q, *k, *v;
+  void *q_out, *k_cache, *v_cache;
+  const long long* slots;
+  const int32_t* positions;  // or nullptr: no rotation (rot = 0)
+  const double* inv_freq;
+  long long qs[2], ks[2], vs[2], qos[2];  // token and head strides in elements
+  long long k_page, v_page;               // page strides of the caches in elements
+  long long n_slots;                      // num_pages * page_size
+  int T, H, H_kv, d, rot;                 // H = 0 without queries
+  int n_rot, n_units;
+  int tb, n_hchunks, hc;                  // tokens per block; the H + 2 H_kv head rows per block
+  int page_shift;
+  float mag;
+};
+
+// One block takes tb tokens and hc of their H + 2 H_kv head rows (queries, keys, values): one
+// cos/sin table, one launch for all three tensors.  Bound by the launch and two dependent loads
+// at a decode step's size, by HBM at a prompt's.
+template <typename T, int V, bool IL>
+__global__ void __launch_bounds__(ROPE_THREADS) fa_paged_append_kernel(const AppendParams p) {
+  __shared__ float2 table[ROPE_TABLE];
+  const int half = p.rot / 2;
+  const int tblk = static_cast<int>(blockIdx.x) / p.n_hchunks;
+  const int hblk = static_cast<int>(blockIdx.x) - tblk * p.n_hchunks;
+  const int n0 = tblk * p.tb, h0 = hblk * p.hc;
+  const int nt = min(p.tb, p.T - n0), nh = min(p.hc, p.H + 2 * p.H_kv - h0);
+  const int total = nt * nh * p.n_units;
+  using Vec = RopeVec<T, V>;
+  for (int e = threadIdx.x; e < nt * half; e += ROPE_THREADS) {
+    const int t = e / half, i = e - t * half;
+    table[e] = rope_cos_sin(p.positions[n0 + t], p.inv_freq[i], p.mag, 1.0f);
+  }
+  __syncthreads();
+  constexpr int DEPTH = 2;
+  for (int e0 = threadIdx.x; e0 < total; e0 += DEPTH * ROPE_THREADS) {
+    Vec va[DEPTH], vb[DEPTH];
+    int c0[DEPTH], c1[DEPTH], ti[DEPTH];
+    T* dst[DEPTH];
+    bool turn[DEPTH];
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k) {
+      const int e = e0 + k * ROPE_THREADS;
+      dst[k] = nullptr;
+      if (e >= total) continue;
+      const int r = e / p.n_units;
+      const int u = e - r * p.n_units;
+      const int t = r / nh;
+      const int hv = h0 + r - t * nh;  // head row: queries, then keys, then values
+      const long long tok = n0 + t;
+      rope_unit<V, IL>(u, p.n_rot, p.rot, c0[k], c1[k]);
+      ti[k] = t * half + u * V;
+      const T* src;
+      if (hv < p.H) {
+        src = static_cast<const T*>(p.q) + tok * p.qs[0] + hv * p.qs[1];
+        dst[k] = static_cast<T*>(p.q_out) + tok * p.qos[0] + hv * p.qos[1];
+        turn[k] = true;
+      } else {
+        const bool is_v = hv >= p.H + p.H_kv;
+        const int h = hv - p.H - (is_v ? p.H_kv : 0);
+        const long long slot = p.slots[tok];
+        if (slot < 0 || slot >= p.n_slots) continue;  // padding, or no such slot
+        const long long pg = slot >> p.page_shift;
+        const long long row = (static_cast<long long>(h) << p.page_shift) +
+                              (slot & ((1 << p.page_shift) - 1));
+        src = is_v ? static_cast<const T*>(p.v) + tok * p.vs[0] + h * p.vs[1]
+                   : static_cast<const T*>(p.k) + tok * p.ks[0] + h * p.ks[1];
+        dst[k] = (is_v ? static_cast<T*>(p.v_cache) + pg * p.v_page
+                       : static_cast<T*>(p.k_cache) + pg * p.k_page) + row * p.d;
+        turn[k] = !is_v;
+      }
+      va[k] = *reinterpret_cast<const Vec*>(src + c0[k]);
+      if (c1[k] >= 0) vb[k] = *reinterpret_cast<const Vec*>(src + c1[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < DEPTH; ++k) {
+      if (dst[k] == nullptr) continue;
+      if (c1[k] >= 0) {
+        if (turn[k]) rope_turn<T, V, IL>(va[k], vb[k], table + ti[k]);
+        *reinterpret_cast<Vec*>(dst[k] + c1[k]) = vb[k];
+      }
+      *reinterpret_cast<Vec*>(dst[k] + c0[k]) = va[k];
+    }
+  }
+}
+
+}  // namespace fa

@@ -178,6 +178,110 @@ int fa_bwd_deterministic_ex(const void* q, const void* k, const void* v, const v
                             const uint8_t* block_mask, const int32_t* kv_len, int dtype,
                             void* workspace, size_t workspace_bytes, int options, void* stream);
 
+/* Options of fa_rope and fa_paged_append (bits). */
+enum {
+  FA_ROPE_INTERLEAVED = 1, /* pairs are columns (2i, 2i+1); else (i, i + rotary_dim/2)     */
+  FA_ROPE_BACKWARD = 2     /* the transposed rotation: the gradient (fa_rope only)          */
+};
+
+/*
+ * fa_rope -- rotary positions on a query or key tensor, and their gradient.  The pages have no
+ * counterpart: it is the position encoding that decoders put between the projections and fa_fwd.
+ *   x, y        [B][H][N][d] of `dtype` with element strides x_strides / y_strides of (b, h, n)
+ *               (host arrays of three; d is contiguous).  Any strides for x (0 broadcasts); y's
+ *               must not be 0 along an extent above 1.  y may be x (same strides); other overlap
+ *               is undefined.  A packed batch [T][H][d] is B = 1, N = T.
+ *   positions   device int32 [B][N] with batch stride positions_stride (0: one row for all), or
+ *               NULL for 0 .. N-1.
+ *   inv_freq    device double [rotary_dim / 2], radians per position.  The angle is formed and
+ *               reduced in fp64, so far positions keep their accuracy.
+ *   Computes, for each pair (x1, x2) of the first rotary_dim columns (even, 2 .. d) with angle a,
+ *       y1 = magnitude (x1 cos a - x2 sin a),   y2 = magnitude (x2 cos a + x1 sin a),
+ *   in fp32, rounded once; the other columns are copied.  FA_ROPE_BACKWARD turns the sign of a:
+ *   y = dL/dx from x = dL/dy.  d <= 1024; B = 0 or N = 0 does nothing.  Rows that allow 16-byte
+ *   accesses take a vector path, others an element path with the same results.
+ */
+int fa_rope(const void* x, void* y, const int32_t* positions, const double* inv_freq, int B, int H,
+            int N, int d, int rotary_dim, const int64_t* x_strides, const int64_t* y_strides,
+            int64_t positions_stride, float magnitude, int options, int dtype, void* stream);
+
+/*
+ * The paged cache.  The pages have no counterpart: these entry points serve a batch of requests
+ * whose keys and values live in pages of one pool.
+ *   Cache      k_cache, v_cache are [num_pages][H_kv][page_size][d] with a free page stride (in
+ *              elements); page_size is a power of two in [16, 1024].  Position p of request b is
+ *              row p % page_size of page block_table[b][p / page_size]; its slot is the number
+ *              page * page_size + p % page_size.
+ *   Batch      the new tokens of all requests are packed: request b owns rows cu_q[b] ..
+ *              cu_q[b+1] - 1 of [T][heads][d] tensors, and they are the last positions of its
+ *              kv_len[b] keys.  Rows behind cu_q[B] are padding.
+ *   The lengths are read on the device only, so a captured graph follows them.
+ *
+ * fa_paged_plan -- one step's bookkeeping from the requests' lengths, in one launch.
+ *   ctx_len, new_len  int32 [B]: cached and new tokens (negative counts as 0).
+ *   free_pages        int32 [n_free]; pages are handed out in order from *cursor on (cursor: one
+ *                     device int32, or NULL for 0), to the requests in order.
+ *   block_table       int32 [B][max_pages], row stride table_stride: entries of pages that begin
+ *                     in this step are written (ceil(ctx / page_size) on), the others are read.
+ *   cu_q [B+1], kv_len [B], positions [max_tokens], slots [max_tokens] (int64), counts [4]:
+ *       counts = {new tokens asked for, pages taken, pages short, cursor after}.
+ *   Tokens beyond max_tokens are left out of the step (of cu_q and kv_len as well).  A token whose
+ *   page is missing (none left, or beyond max_pages, or a negative id) gets slot -1; an entry for
+ *   which no page was left becomes -1.  Padding gets position 0, slot -1.
+ */
+int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t* free_pages,
+                  int n_free, const int32_t* cursor, int32_t* block_table, int64_t table_stride,
+                  int B, int max_pages, int page_size, int max_tokens, int32_t* cu_q,
+                  int32_t* kv_len, int32_t* positions, int64_t* slots, int32_t* counts,
+                  void* stream);
+
+/*
+ * fa_paged_append -- writes T tokens' keys and values to their slots, and with inv_freq rotates
+ * the keys on the way (as fa_rope does) and the queries into q_out, all in one launch.
+ *   q, q_out [T][H][d] (H = 0: none), k, v [T][H_kv][d]; strides = the token and head strides of
+ *   q, k, v, q_out in elements (host array of eight; d contiguous).  q_out may be q.
+ *   inv_freq   NULL (rotary_dim 0, positions unused): keys are copied, q (if any) is copied.
+ *   slots      a token with a slot outside [0, num_pages * page_size) is not stored.  The slots
+ *              stored to must differ; for a slot named twice it is not defined which values land.
+ *   options    FA_ROPE_INTERLEAVED or 0.  d <= 1024; any alignment (element path as in fa_rope).
+ */
+int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
+                    void* v_cache, const int64_t* slots, const int32_t* positions,
+                    const double* inv_freq, int T, int H, int H_kv, int d, int rotary_dim,
+                    const int64_t* strides, int64_t k_page_stride, int64_t v_page_stride,
+                    int page_size, int num_pages, float magnitude, int options, int dtype,
+                    void* stream);
+
+/* Bytes of workspace fa_paged_fwd needs (0 for sizes it rejects). */
+size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d);
+
+/*
+ * fa_paged_fwd -- attention of each request's new tokens over its paged cache, grouped heads as
+ * in fa_fwd_gqa: O = softmax(scale Q K^T, masked) V and lse, decoding steps and prompt chunks in
+ * any mix.
+ *   q [T][H][d] (token and head strides in elements), o [T][H][d] and lse [T][H] contiguous.
+ *   Masks      token i of a request with nq new tokens sees the keys j < kv_len[b] with, causal
+ *              != 0, j <= kv_len[b] - nq + i.  A key whose block-table entry is outside
+ *              [0, num_pages) is masked.  A row with no key gets O = 0, lse = -inf.  What stale
+ *              rows of a page hold (NaN included) does not matter.
+ *   Lengths    cu_q is clamped to [0, T] and kv_len to [0, max_pages * page_size].  Rows of o
+ *              and lse that no request owns are left as they were.
+ *   max_q      the most new tokens of any request, as a hint for the choice of kernel only (every
+ *              kernel takes every length); <= 0: the mean.
+ *   dtype      FA_BF16: d in {64, 128}; q's and the pages' strides multiples of 8 elements.
+ *              FA_F32: 1 <= d <= 128; CUDA cores, fp32 throughout.
+ *   workspace  device memory of at least fa_paged_workspace_size() bytes, 256-byte aligned, scratch
+ *              only.  Calls that may overlap on the GPU need one each.
+ *   T = 0 does nothing.  Results do not vary between runs.
+ */
+int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
+                 const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_q, void* o,
+                 float* lse, int T, int B, int H, int H_kv, int d, int64_t q_token_stride,
+                 int64_t q_head_stride, int64_t k_page_stride, int64_t v_page_stride,
+                 int64_t table_stride, int page_size, int num_pages, int max_pages, int max_q,
+                 float scale, int causal, int dtype, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
 /* Flags of fa_fwd_tile_reference: the other two axes of the deviation study. */
 enum {
   FA_TILE_REVERSE = 1,    /* visit the key tiles from the last to the first */
