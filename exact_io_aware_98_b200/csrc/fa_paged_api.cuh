@@ -82,9 +82,11 @@ PagedShape simt_shape(bool few, int d) {
   return {few ? 8 : 32, kSms * per_sm};
 }
 
+PagedShape decode_shape() { return {16, kSms}; }
+
 size_t paged_ws_bytes(long long T, int group, int d) {
   size_t n = 0;
-  for (const PagedShape v : {simt_shape(true, d), simt_shape(false, d)})
+  for (const PagedShape v : {simt_shape(true, d), simt_shape(false, d), decode_shape()})
     n = std::max(n, paged_ws_part(T, group, d, v, nullptr, nullptr, nullptr));
   return n;
 }
@@ -131,6 +133,47 @@ int launch_paged_simt(fa::PagedParams p, int H_kv, void* ws, cudaStream_t s) {
   fa::fa_paged_simt_kernel<T, WR, WK><<<v.ctas, 128, smem, s>>>(p);
   if ((rc = check_launch("fa_paged_simt_kernel")) != FA_OK) return rc;
   return launch_join<T>(p, v.ctas, s);
+}
+
+// 4-D view [page][H_kv][page_size][d] bf16 of a cache, 128-byte swizzled boxes of 64 columns and
+// box_rows rows of one page and head.  An out-of-range page reads as zeros.
+int make_cache_map(CUtensorMap* map, const void* base, int pages, int H_kv, int page_size, int d,
+                   long long page_stride, int box_rows, const char* name) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const long long page_elems = static_cast<long long>(H_kv) * page_size * d;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
+                              static_cast<cuuint64_t>(H_kv), static_cast<cuuint64_t>(pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2,
+                                 static_cast<cuuint64_t>(page_size) * d * 2,
+                                 static_cast<cuuint64_t>(pages > 1 ? page_stride : page_elems) * 2};
+  const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_rows), 1u, 1u};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "tensor map for %s failed (%d)", name, (int)r);
+  return FA_OK;
+}
+
+template <int D>
+int launch_paged_decode(fa::PagedParams p, int H_kv, int page_size, void* ws, cudaStream_t s) {
+  using L = fa::PagedDecodeLayout<D>;
+  const PagedShape v = decode_shape();
+  paged_tiles(p, v, H_kv, ws);
+  CUtensorMap mk, mv;
+  const int box = std::min(page_size, L::KT);
+  int rc;
+  if ((rc = make_cache_map(&mk, p.k, p.num_pages, H_kv, page_size, D, p.k_page, box, "k_cache")) != FA_OK) return rc;
+  if ((rc = make_cache_map(&mv, p.v, p.num_pages, H_kv, page_size, D, p.v_page, box, "v_cache")) != FA_OK) return rc;
+  if ((rc = set_smem(fa::fa_paged_decode_sm100_kernel<D>, L::SMEM_ALLOC)) != FA_OK) return rc;
+  {
+    TimedLaunch tl("fa_paged_decode_sm100_kernel", s);
+    fa::fa_paged_decode_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mk, mv, p);
+    if ((rc = check_launch("fa_paged_decode_sm100_kernel")) != FA_OK) return rc;
+  }
+  return launch_join<__nv_bfloat16>(p, v.ctas, s);
 }
 
 }  // namespace
@@ -404,6 +447,9 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // new tokens per request: the caller's bound, or the batch's mean
   const long long rows = static_cast<long long>(max_q > 0 ? std::min(max_q, T) : (T + B - 1) / B) * p.group;
+  if (dtype == FA_BF16 && rows <= 16)
+    return d == 64 ? launch_paged_decode<64>(p, H_kv, page_size, workspace, s)
+                   : launch_paged_decode<128>(p, H_kv, page_size, workspace, s);
   const bool few = rows <= 8;
   if (dtype == FA_F32)
     return few ? launch_paged_simt<float, 1, 4>(p, H_kv, workspace, s)

@@ -195,6 +195,9 @@ CASES = [
     (LONG, 8, 2, 128, 16, "bf16", True, 3),          # one request over all SMs
     (LONG, 4, 1, 64, 64, "bf16", True, 3),
     (LONG, 40, 2, 128, 64, "bf16", True, None),
+    ([(1, 20000)] * 6, 2, 2, 128, 64, "bf16", True, 1),  # many key tiles per SM
+    ([(1, 30000)] * 6, 4, 2, 64, 16, "bf16", True, 1),
+    ([(2, 9000), (1, 1)] * 9, 16, 4, 128, 32, "bf16", True, 2),
     ([(300, 4000), (1, 3000), (40, 41)], 8, 2, 128, 16, "bf16", True, 300),
     ([(257, 513)], 2, 2, 64, 16, "bf16", True, 257),
     ([(1, 300)] * 300, 2, 1, 64, 16, "bf16", True, 1),  # many small requests
