@@ -22,6 +22,7 @@
 #include "fa_fwd_sm100.cuh"
 #include "fa_paged.cuh"
 #include "fa_paged_cache.cuh"
+#include "fa_paged_chunk_sm100.cuh"
 #include "fa_paged_decode_sm100.cuh"
 #include "fa_paged_simt.cuh"
 #include "fa_rope.cuh"

@@ -83,10 +83,11 @@ PagedShape simt_shape(bool few, int d) {
 }
 
 PagedShape decode_shape() { return {16, kSms}; }
+PagedShape chunk_shape(int d) { return {256, kSms * (d == 64 ? fa::PagedChunkLayout<64>::CTAS_PER_SM : 1)}; }
 
 size_t paged_ws_bytes(long long T, int group, int d) {
   size_t n = 0;
-  for (const PagedShape v : {simt_shape(true, d), simt_shape(false, d), decode_shape()})
+  for (const PagedShape v : {simt_shape(true, d), simt_shape(false, d), decode_shape(), chunk_shape(d)})
     n = std::max(n, paged_ws_part(T, group, d, v, nullptr, nullptr, nullptr));
   return n;
 }
@@ -172,6 +173,47 @@ int launch_paged_decode(fa::PagedParams p, int H_kv, int page_size, void* ws, cu
     TimedLaunch tl("fa_paged_decode_sm100_kernel", s);
     fa::fa_paged_decode_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mk, mv, p);
     if ((rc = check_launch("fa_paged_decode_sm100_kernel")) != FA_OK) return rc;
+  }
+  return launch_join<__nv_bfloat16>(p, v.ctas, s);
+}
+
+// 3-D view [T][H][d] bf16 of the packed queries, 128-byte swizzled boxes of 64 columns, `heads`
+// heads and `tokens` tokens.
+int make_query_map(CUtensorMap* map, const fa::PagedParams& p, int heads, int tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(p.H),
+                              static_cast<cuuint64_t>(p.T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.H > 1 ? p.q_sh : p.d) * 2,
+                                 static_cast<cuuint64_t>(p.T > 1 ? p.q_st : p.d) * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_CUDA, "tensor map for q failed (%d)", (int)r);
+  return FA_OK;
+}
+
+template <int D>
+int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cudaStream_t s) {
+  using L = fa::PagedChunkLayout<D>;
+  const PagedShape v = chunk_shape(D);
+  paged_tiles(p, v, H_kv, ws);
+  CUtensorMap mq, mqf, mk, mv;
+  const int box = std::min(page_size, L::BN);
+  const int tpt = L::R / p.G, few = std::min(tpt, std::max(1, 32 / p.G));
+  int rc;
+  if ((rc = make_query_map(&mq, p, p.G, tpt)) != FA_OK) return rc;
+  if ((rc = make_query_map(&mqf, p, p.G, few)) != FA_OK) return rc;
+  if ((rc = make_cache_map(&mk, p.k, p.num_pages, H_kv, page_size, D, p.k_page, box, "k_cache")) != FA_OK) return rc;
+  if ((rc = make_cache_map(&mv, p.v, p.num_pages, H_kv, page_size, D, p.v_page, box, "v_cache")) != FA_OK) return rc;
+  if ((rc = set_smem(fa::fa_paged_chunk_sm100_kernel<D>, L::SMEM_ALLOC)) != FA_OK) return rc;
+  {
+    TimedLaunch tl("fa_paged_chunk_sm100_kernel", s);
+    fa::fa_paged_chunk_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mq, mqf, mk, mv, few, p);
+    if ((rc = check_launch("fa_paged_chunk_sm100_kernel")) != FA_OK) return rc;
   }
   return launch_join<__nv_bfloat16>(p, v.ctas, s);
 }
@@ -404,6 +446,8 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
   const long long page_elems = static_cast<long long>(H_kv) * page_size * d;
   if (num_pages > 1 && (k_page_stride < page_elems || v_page_stride < page_elems))
     return fail(FA_ERR_INVALID, "cache pages overlap");
+  if ((T > 1 && q_token_stride < 1) || (H > 1 && q_head_stride < 1))
+    return fail(FA_ERR_INVALID, "q's strides must be positive");
   if (T == 0) return FA_OK;
   if (!q || !k_cache || !v_cache || !block_table || !kv_len || !cu_q || !o || !lse)
     return fail(FA_ERR_INVALID, "null tensor pointer");
@@ -447,15 +491,15 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // new tokens per request: the caller's bound, or the batch's mean
   const long long rows = static_cast<long long>(max_q > 0 ? std::min(max_q, T) : (T + B - 1) / B) * p.group;
-  if (dtype == FA_BF16 && rows <= 16)
-    return d == 64 ? launch_paged_decode<64>(p, H_kv, page_size, workspace, s)
-                   : launch_paged_decode<128>(p, H_kv, page_size, workspace, s);
-  const bool few = rows <= 8;
-  if (dtype == FA_F32)
-    return few ? launch_paged_simt<float, 1, 4>(p, H_kv, workspace, s)
-               : launch_paged_simt<float, 4, 1>(p, H_kv, workspace, s);
-  return few ? launch_paged_simt<__nv_bfloat16, 1, 4>(p, H_kv, workspace, s)
-             : launch_paged_simt<__nv_bfloat16, 4, 1>(p, H_kv, workspace, s);
+  if (dtype == FA_BF16) {
+    if (rows <= 16)
+      return d == 64 ? launch_paged_decode<64>(p, H_kv, page_size, workspace, s)
+                     : launch_paged_decode<128>(p, H_kv, page_size, workspace, s);
+    return d == 64 ? launch_paged_chunk<64>(p, H_kv, page_size, workspace, s)
+                   : launch_paged_chunk<128>(p, H_kv, page_size, workspace, s);
+  }
+  return rows <= 8 ? launch_paged_simt<float, 1, 4>(p, H_kv, workspace, s)
+                   : launch_paged_simt<float, 4, 1>(p, H_kv, workspace, s);
 }
 
 }  // extern "C"
