@@ -46,11 +46,11 @@ struct PagedParams {
   int page_shift, num_pages, max_pages;
   int causal;
   float scale2;                // scale * log2(e)
-  // workspace: headers [ctas], row statistics [ctas][2][rows_cap], sums [ctas][2][rows_cap][d]
-  int4* ws_head;               // two int4 per CTA
+  // workspace: headers [ctas], row statistics [ctas][2][rows_cap], sums [ctas][2][rows_cap][pitch]
+  int4* ws_head;
   float2* ws_ml;
   float* ws_o;
-  int rows_cap;
+  int rows_cap, ws_pitch;      // rows per part; floats per row (d rounded up to 4)
 };
 
 // One row tile of a request, as the CTAs pass it around.
@@ -231,48 +231,88 @@ __device__ __forceinline__ float paged_lse(float m, float l) {
 }
 
 // ---------------------------------------------------------------------------------- join
-// Block (c, j) joins every gridDim.y-th row, from row j, of the item that CTA c left unfinished:
-// O = sum_i 2^(m_i - m) O_i / l, l = sum_i 2^(m_i - m) l_i, over the parts in key order.  One
-// warp per row.  Bound by the launch and two dependent loads when few items are split; launched
-// to overlap the end of the kernel before it.
-constexpr int JOIN_WARPS = 4;
+// Block (c, j) joins rows of the item that CTA c left unfinished: O = sum_i 2^(m_i - m) O_i / l,
+// l = sum_i 2^(m_i - m) l_i, over the parts in key order.  WPR warps share a row: they take every
+// WPR-th part, eight of them loaded at once, and add their sums in warp order.  WPR = 4 where
+// items have few rows and many parts (decoding: 12.2 us for the call of one request of 2000 keys,
+// against 19.7 us with a part's loads waiting for the one before), 1 where they have many rows.
+// Bound by the launch and three dependent loads; launched to overlap the end of the kernel before.
+constexpr int JOIN_WARPS = 8;
 
-template <typename T>
+template <typename T, int WPR>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_kernel(const PagedParams p) {
+  __shared__ float4 s_acc[JOIN_WARPS][32];
+  __shared__ float s_l[JOIN_WARPS];
   grid_dep_wait();
   const int cta = blockIdx.x;
   const int4 head = p.ws_head[cta];
   if (head.x <= 0) return;
-  const int lane = threadIdx.x & 31;
-  const int rows = head.w * p.G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = head.w * p.G, parts = head.x;
   const size_t first = static_cast<size_t>(cta) * 2 + 1;
-  for (int r = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); r < rows;
-       r += JOIN_WARPS * gridDim.y) {
+  constexpr int AT_ONCE = JOIN_WARPS / WPR;
+  for (int r0 = blockIdx.y * AT_ONCE; r0 < rows; r0 += gridDim.y * AT_ONCE) {
+    const int r = r0 + warp / WPR;
     const int qh = paged_row_head(p, head.y, r, rows);
-    if (qh < 0) continue;
-    float m = -INFINITY;
-    for (int i = lane; i < head.x; i += 32)  // part i: slot 1 of this CTA, slot 0 of the others
-      m = fmaxf(m, p.ws_ml[(i == 0 ? first : first + 2 * i - 1) * p.rows_cap + r].x);
+    // part i: slot 1 of this CTA, then slot 0 of the ones after it
+    auto stats = [&](int i) { return (i == 0 ? first : first + 2 * i - 1) * p.rows_cap + r; };
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);  // columns 4 lane ..
+    if (qh >= 0) {
+      for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.ws_ml[stats(i)].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < head.x; ++i) {
-      const size_t slot = i == 0 ? first : first + 2 * i - 1;
-      const float2 ml = p.ws_ml[slot * p.rows_cap + r];
-      if (ml.x == -INFINITY) continue;
-      const float w = exp2f(ml.x - m);
-      l = fmaf(w, ml.y, l);
-      const float* part = p.ws_o + (slot * p.rows_cap + r) * p.d;
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      constexpr int DEPTH = 8;
+      for (int i0 = warp % WPR; i0 < parts; i0 += DEPTH * WPR) {
+        float4 part[DEPTH];
+        float2 ml[DEPTH];
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k) {
+          const int i = i0 + k * WPR;
+          if (i >= parts) continue;
+          ml[k] = p.ws_ml[stats(i)];
+          const float* src = p.ws_o + stats(i) * p.ws_pitch + 4 * lane;
+          part[k] = 4 * lane < p.d ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < DEPTH; ++k) {
+          if (i0 + k * WPR >= parts || ml[k].x == -INFINITY) continue;
+          const float w = exp2f(ml[k].x - m);
+          l = fmaf(w, ml[k].y, l);
+          acc.x = fmaf(w, part[k].x, acc.x);
+          acc.y = fmaf(w, part[k].y, acc.y);
+          acc.z = fmaf(w, part[k].z, acc.z);
+          acc.w = fmaf(w, part[k].w, acc.w);
+        }
+      }
+    }
+    if constexpr (WPR > 1) {
+      s_acc[warp][lane] = acc;
+      if (lane == 0) s_l[warp] = l;
+      __syncthreads();
+      if (warp % WPR == 0) {
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) {
+          const float4 a = s_acc[warp + w][lane];
+          acc.x += a.x;
+          acc.y += a.y;
+          acc.z += a.z;
+          acc.w += a.w;
+          l += s_l[warp + w];
+        }
+      }
+      __syncthreads();  // s_acc is rewritten for the next rows
+    }
+    if (qh >= 0 && warp % WPR == 0) {
+      const long long row = static_cast<long long>(head.z + r / p.G) * p.H + qh;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
+      T* op = static_cast<T*>(p.o) + row * p.d + 4 * lane;
+      const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (32 * c + lane < p.d) acc[c] = fmaf(w, part[32 * c + lane], acc[c]);
+        if (4 * lane + c < p.d) op[c] = from_f<T>(o[c]);
+      if (lane == 0) p.lse[row] = paged_lse(m, l);
     }
-    const float inv = l == 0.f ? 0.0f : 1.0f / l;
-    const long long row = static_cast<long long>(head.z + r / p.G) * p.H + qh;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (32 * c + lane < p.d) static_cast<T*>(p.o)[row * p.d + 32 * c + lane] = from_f<T>(acc[c] * inv);
-    if (lane == 0) p.lse[row] = paged_lse(m, l);
   }
 }
 

@@ -27,22 +27,26 @@ int rope_vec(int es, int d, int rot, bool rows16) {
   return rows16 && (rot / 2) % v == 0 && (d - rot) % v == 0 ? v : 1;
 }
 
-// Tokens and heads per block: about four 16-byte pairs per thread, fewer while the grid would
-// leave SMs without two blocks.
-void rope_tiles(long long N, int H, int B, int units, int half, int* tb, int* hc) {
-  const int want = 4 * fa::ROPE_THREADS;
-  int h = std::max(1, std::min(H, want / std::max(1, units)));
-  int t = std::max(1, want / std::max(1, units * h));
-  if (half > 0) t = std::min(t, fa::ROPE_TABLE / half);
-  t = static_cast<int>(std::min<long long>(t, N));
-  auto blocks = [&]() { return ((N + t - 1) / t) * ((H + h - 1) / h) * B; };
-  while (blocks() < 2 * kSms && static_cast<long long>(t) * h * units > fa::ROPE_THREADS) {
-    if (t > 1) t = (t + 1) / 2;
-    else if (h > 1) h = (h + 1) / 2;
-    else break;
-  }
-  *tb = t;
-  *hc = h;
+// Lays blocks over the work.  A thread walks over several heads where that still leaves every SM
+// enough blocks; otherwise one head per thread, and so few tokens per block that the table of cos
+// and sin is one entry per thread.
+fa::RopeShape rope_shape(long long N, int heads, int B, int units, int pass, int half) {
+  fa::RopeShape sh;
+  sh.pass = pass;
+  sh.uw = std::min(units, fa::ROPE_THREADS);
+  sh.u_blocks = (units + sh.uw - 1) / sh.uw;
+  const int rows = fa::ROPE_THREADS / sh.uw;
+  auto place = [&](int tb, int hpt) {
+    sh.tb = static_cast<int>(std::min<long long>(N, std::max(1, std::min(tb, rows))));
+    sh.hs = std::min(heads, rows / sh.tb);
+    sh.hpt = std::min(hpt, (heads + sh.hs - 1) / sh.hs);
+    sh.h_blocks = (heads + sh.hs * sh.hpt - 1) / (sh.hs * sh.hpt);
+    return (N + sh.tb - 1) / sh.tb * sh.h_blocks * sh.u_blocks * B;
+  };
+  if (place(rows, 2 * fa::ROPE_DEPTH) >= 6 * kSms) return sh;
+  if (place(rows, fa::ROPE_DEPTH) >= 3 * kSms / 2) return sh;
+  place(half > 0 ? fa::ROPE_THREADS / half : rows, 1);
+  return sh;
 }
 
 template <typename T, int V>
@@ -64,7 +68,7 @@ size_t paged_ws_part(long long T, int group, int d, PagedShape v, int* rows_cap,
                      size_t* off_o) {
   const int splits = (group + v.rows - 1) / v.rows;
   const int G = (group + splits - 1) / splits;
-  const long long cap = std::min<long long>(v.rows, (T * G + 7) / 8 * 8);
+  const long long cap = std::min<long long>(v.rows, T * G);
   const size_t head = round256(static_cast<size_t>(v.ctas) * sizeof(int4));
   const size_t ml = round256(static_cast<size_t>(v.ctas) * 2 * cap * sizeof(float2));
   if (rows_cap != nullptr) {
@@ -72,7 +76,7 @@ size_t paged_ws_part(long long T, int group, int d, PagedShape v, int* rows_cap,
     *off_ml = head;
     *off_o = head + ml;
   }
-  return head + ml + round256(static_cast<size_t>(v.ctas) * 2 * cap * d * sizeof(float));
+  return head + ml + round256(static_cast<size_t>(v.ctas) * 2 * cap * ((d + 3) / 4 * 4) * sizeof(float));
 }
 
 // CTAs of a CUDA-core variant: what shared memory lets an SM hold, up to four.
@@ -92,12 +96,12 @@ size_t paged_ws_bytes(long long T, int group, int d) {
   return n;
 }
 
-template <typename T>
+// WPR: warps per row of a split item.
+template <typename T, int WPR>
 int launch_join(const fa::PagedParams& p, int ctas, cudaStream_t s) {
-  // blocks per split item: a warp per row
-  const int by = (p.rows_cap + fa::JOIN_WARPS - 1) / fa::JOIN_WARPS;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, std::min(by, 16));
+  const int at_once = fa::JOIN_WARPS / WPR;
+  cfg.gridDim = dim3(ctas, std::min((p.rows_cap + at_once - 1) / at_once, 16));
   cfg.blockDim = dim3(fa::JOIN_WARPS * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -105,7 +109,7 @@ int launch_join(const fa::PagedParams& p, int ctas, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::fa_paged_join_kernel<T>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::fa_paged_join_kernel<T, WPR>, p);
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "fa_paged_join_kernel: %s", cudaGetErrorString(e));
   return check_launch("fa_paged_join_kernel");
 }
@@ -116,6 +120,7 @@ void paged_tiles(fa::PagedParams& p, PagedShape v, int H_kv, void* ws) {
   p.splits = (p.group + v.rows - 1) / v.rows;
   p.G = (p.group + p.splits - 1) / p.splits;
   p.Hv = H_kv * p.splits;
+  p.ws_pitch = (p.d + 3) / 4 * 4;
   paged_ws_part(p.T, p.group, p.d, v, &p.rows_cap, &off_ml, &off_o);
   uint8_t* b = static_cast<uint8_t*>(ws);
   p.ws_head = reinterpret_cast<int4*>(b);
@@ -133,7 +138,7 @@ int launch_paged_simt(fa::PagedParams p, int H_kv, void* ws, cudaStream_t s) {
   if (rc != FA_OK) return rc;
   fa::fa_paged_simt_kernel<T, WR, WK><<<v.ctas, 128, smem, s>>>(p);
   if ((rc = check_launch("fa_paged_simt_kernel")) != FA_OK) return rc;
-  return launch_join<T>(p, v.ctas, s);
+  return launch_join<T, (WK > 1 ? 4 : 1)>(p, v.ctas, s);
 }
 
 // 4-D view [page][H_kv][page_size][d] bf16 of a cache, 128-byte swizzled boxes of 64 columns and
@@ -174,7 +179,7 @@ int launch_paged_decode(fa::PagedParams p, int H_kv, int page_size, void* ws, cu
     fa::fa_paged_decode_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mk, mv, p);
     if ((rc = check_launch("fa_paged_decode_sm100_kernel")) != FA_OK) return rc;
   }
-  return launch_join<__nv_bfloat16>(p, v.ctas, s);
+  return launch_join<__nv_bfloat16, 4>(p, v.ctas, s);
 }
 
 // 3-D view [T][H][d] bf16 of the packed queries, 128-byte swizzled boxes of 64 columns, `heads`
@@ -215,7 +220,7 @@ int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cud
     fa::fa_paged_chunk_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mq, mqf, mk, mv, few, p);
     if ((rc = check_launch("fa_paged_chunk_sm100_kernel")) != FA_OK) return rc;
   }
-  return launch_join<__nv_bfloat16>(p, v.ctas, s);
+  return launch_join<__nv_bfloat16, 1>(p, v.ctas, s);
 }
 
 }  // namespace
@@ -266,18 +271,20 @@ int fa_rope(const void* x, void* y, const int32_t* positions, const double* inv_
   p.rot = rotary_dim;
   const int V = rope_vec(es, d, rotary_dim, rows16);
   p.n_rot = rotary_dim / 2 / V;
-  p.n_units = p.n_rot + (x == y ? 0 : (d - rotary_dim) / V);  // in place, the rest stays
-  p.heads_inner = std::llabs(x_strides[1]) < std::llabs(x_strides[2]) ? 1 : 0;
-  rope_tiles(N, H, B, p.n_units, rotary_dim / 2, &p.tb, &p.hc);
-  p.n_hchunks = (H + p.hc - 1) / p.hc;
+  const int vecs = x == y ? 0 : (d - rotary_dim) / V;  // pass-through; in place, they stay
+  const int pass = vecs % 2 == 0 ? 2 : 1;
+  p.n_units = p.n_rot + vecs / pass;
+  p.shape = rope_shape(N, H, B, p.n_units, pass, rotary_dim / 2);
   p.mag = magnitude;
   p.sgn = (options & FA_ROPE_BACKWARD) ? -1.0f : 1.0f;
-  const long long gx = static_cast<long long>((N + p.tb - 1) / p.tb) * p.n_hchunks;
+  const long long gx = (N + p.shape.tb - 1ll) / p.shape.tb * p.shape.h_blocks * p.shape.u_blocks;
   if (gx > 0x7fffffffll) return fail(FA_ERR_UNSUPPORTED, "grid too large");
   const bool il = (options & FA_ROPE_INTERLEAVED) != 0;
   auto* kern = dtype == FA_BF16 ? (V > 1 ? rope_kernel<__nv_bfloat16, 8>(il) : rope_kernel<__nv_bfloat16, 1>(il))
                                 : (V > 1 ? rope_kernel<float, 4>(il) : rope_kernel<float, 1>(il));
-  kern<<<dim3(static_cast<unsigned>(gx), std::min(B, 65535)), fa::ROPE_THREADS, 0,
+  const int by = std::min(B, 65535);
+  if ((B + by - 1) / by > 65535) return fail(FA_ERR_UNSUPPORTED, "B too large");
+  kern<<<dim3(static_cast<unsigned>(gx), by, (B + by - 1) / by), fa::ROPE_THREADS, 0,
          static_cast<cudaStream_t>(stream)>>>(p);
   return check_launch("fa_rope_kernel");
 }
@@ -398,13 +405,13 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
   p.rot = rotary_dim;
   const int V = rope_vec(es, d, rotary_dim, rows16);
   p.n_rot = rotary_dim / 2 / V;
-  p.n_units = p.n_rot + (d - rotary_dim) / V;
+  const int vecs = (d - rotary_dim) / V, pass = vecs % 2 == 0 ? 2 : 1;
+  p.n_units = p.n_rot + vecs / pass;
   p.page_shift = shift;
   p.mag = magnitude;
   const int rows = H + 2 * H_kv;
-  rope_tiles(T, rows, 1, p.n_units, rotary_dim / 2, &p.tb, &p.hc);
-  p.n_hchunks = (rows + p.hc - 1) / p.hc;
-  const long long gx = static_cast<long long>((T + p.tb - 1) / p.tb) * p.n_hchunks;
+  p.shape = rope_shape(T, rows, 1, p.n_units, pass, rotary_dim / 2);
+  const long long gx = (T + p.shape.tb - 1ll) / p.shape.tb * p.shape.h_blocks * p.shape.u_blocks;
   if (gx > 0x7fffffffll) return fail(FA_ERR_UNSUPPORTED, "grid too large");
   const bool il = (options & FA_ROPE_INTERLEAVED) != 0;
   auto* kern = dtype == FA_BF16 ? (V > 1 ? append_kernel<__nv_bfloat16, 8>(il) : append_kernel<__nv_bfloat16, 1>(il))

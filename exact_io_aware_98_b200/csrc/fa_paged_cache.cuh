@@ -155,79 +155,52 @@ struct AppendParams {
   long long n_slots;                      // num_pages * page_size
   int T, H, H_kv, d, rot;                 // H = 0 without queries
   int n_rot, n_units;
-  int tb, n_hchunks, hc;                  // tokens per block; the H + 2 H_kv head rows per block
+  RopeShape shape;
   int page_shift;
   float mag;
 };
 
-// One block takes tb tokens and hc of their H + 2 H_kv head rows (queries, keys, values): one
-// cos/sin table, one launch for all three tensors.  Bound by the launch and two dependent loads
-// at a decode step's size, by HBM at a prompt's.
+// The H + 2 H_kv head rows of a token: queries, keys, values.
+template <typename T>
+struct AppendRows {
+  const AppendParams& p;
+  const T *q, *k, *v;   // the token's first rows
+  T *qo, *kc, *vc;      // where they go; kc = nullptr: the token is not stored
+  __device__ __forceinline__ void prepare(int n) {
+    q = static_cast<const T*>(p.q) + n * p.qs[0];
+    qo = static_cast<T*>(p.q_out) + n * p.qos[0];
+    k = static_cast<const T*>(p.k) + n * p.ks[0];
+    v = static_cast<const T*>(p.v) + n * p.vs[0];
+    const long long slot = p.slots[n];
+    kc = vc = nullptr;
+    if (slot >= 0 && slot < p.n_slots) {  // else padding, or no such slot
+      const long long pg = slot >> p.page_shift, row = slot & ((1 << p.page_shift) - 1);
+      kc = static_cast<T*>(p.k_cache) + pg * p.k_page + row * p.d;
+      vc = static_cast<T*>(p.v_cache) + pg * p.v_page + row * p.d;
+    }
+  }
+  __device__ __forceinline__ const T* src(int h) const {
+    if (h < p.H) return q + h * p.qs[1];
+    h -= p.H;
+    return h < p.H_kv ? k + h * p.ks[1] : v + (h - p.H_kv) * p.vs[1];
+  }
+  __device__ __forceinline__ T* dst(int h) const {
+    if (h < p.H) return qo + h * p.qos[1];
+    h -= p.H;
+    return h < p.H_kv ? kc + (static_cast<long long>(h) << p.page_shift) * p.d
+                      : vc + (static_cast<long long>(h - p.H_kv) << p.page_shift) * p.d;
+  }
+  __device__ __forceinline__ bool stored(int h) const { return h < p.H || kc != nullptr; }
+  __device__ __forceinline__ bool turned(int h) const { return h < p.H + p.H_kv; }
+};
+
+// One launch for all three tensors.  Bound by the launch and two dependent loads at a decode
+// step's size, by HBM at a prompt's.
 template <typename T, int V, bool IL>
-__global__ void __launch_bounds__(ROPE_THREADS) fa_paged_append_kernel(const AppendParams p) {
-  __shared__ float2 table[ROPE_TABLE];
-  const int half = p.rot / 2;
-  const int tblk = static_cast<int>(blockIdx.x) / p.n_hchunks;
-  const int hblk = static_cast<int>(blockIdx.x) - tblk * p.n_hchunks;
-  const int n0 = tblk * p.tb, h0 = hblk * p.hc;
-  const int nt = min(p.tb, p.T - n0), nh = min(p.hc, p.H + 2 * p.H_kv - h0);
-  const int total = nt * nh * p.n_units;
-  using Vec = RopeVec<T, V>;
-  for (int e = threadIdx.x; e < nt * half; e += ROPE_THREADS) {
-    const int t = e / half, i = e - t * half;
-    table[e] = rope_cos_sin(p.positions[n0 + t], p.inv_freq[i], p.mag, 1.0f);
-  }
-  __syncthreads();
-  constexpr int DEPTH = 2;
-  for (int e0 = threadIdx.x; e0 < total; e0 += DEPTH * ROPE_THREADS) {
-    Vec va[DEPTH], vb[DEPTH];
-    int c0[DEPTH], c1[DEPTH], ti[DEPTH];
-    T* dst[DEPTH];
-    bool turn[DEPTH];
-#pragma unroll
-    for (int k = 0; k < DEPTH; ++k) {
-      const int e = e0 + k * ROPE_THREADS;
-      dst[k] = nullptr;
-      if (e >= total) continue;
-      const int r = e / p.n_units;
-      const int u = e - r * p.n_units;
-      const int t = r / nh;
-      const int hv = h0 + r - t * nh;  // head row: queries, then keys, then values
-      const long long tok = n0 + t;
-      rope_unit<V, IL>(u, p.n_rot, p.rot, c0[k], c1[k]);
-      ti[k] = t * half + u * V;
-      const T* src;
-      if (hv < p.H) {
-        src = static_cast<const T*>(p.q) + tok * p.qs[0] + hv * p.qs[1];
-        dst[k] = static_cast<T*>(p.q_out) + tok * p.qos[0] + hv * p.qos[1];
-        turn[k] = true;
-      } else {
-        const bool is_v = hv >= p.H + p.H_kv;
-        const int h = hv - p.H - (is_v ? p.H_kv : 0);
-        const long long slot = p.slots[tok];
-        if (slot < 0 || slot >= p.n_slots) continue;  // padding, or no such slot
-        const long long pg = slot >> p.page_shift;
-        const long long row = (static_cast<long long>(h) << p.page_shift) +
-                              (slot & ((1 << p.page_shift) - 1));
-        src = is_v ? static_cast<const T*>(p.v) + tok * p.vs[0] + h * p.vs[1]
-                   : static_cast<const T*>(p.k) + tok * p.ks[0] + h * p.ks[1];
-        dst[k] = (is_v ? static_cast<T*>(p.v_cache) + pg * p.v_page
-                       : static_cast<T*>(p.k_cache) + pg * p.k_page) + row * p.d;
-        turn[k] = !is_v;
-      }
-      va[k] = *reinterpret_cast<const Vec*>(src + c0[k]);
-      if (c1[k] >= 0) vb[k] = *reinterpret_cast<const Vec*>(src + c1[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < DEPTH; ++k) {
-      if (dst[k] == nullptr) continue;
-      if (c1[k] >= 0) {
-        if (turn[k]) rope_turn<T, V, IL>(va[k], vb[k], table + ti[k]);
-        *reinterpret_cast<Vec*>(dst[k] + c1[k]) = vb[k];
-      }
-      *reinterpret_cast<Vec*>(dst[k] + c0[k]) = va[k];
-    }
-  }
+__global__ void __launch_bounds__(ROPE_THREADS, 3) fa_paged_append_kernel(const AppendParams p) {
+  AppendRows<T> rows = {p, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
+  rope_block<T, V, IL>(p.shape, p.T, p.H + 2 * p.H_kv, p.rot, p.n_rot, p.n_units, p.positions,
+                       p.inv_freq, p.mag, 1.0f, rows);
 }
 
 }  // namespace fa

@@ -538,7 +538,7 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
                   dst[i] = make_uint4(hh[0], hh[1], hh[2], hh[3]);
                 }
               } else {
-                uint4* dst = reinterpret_cast<uint4*>(p.ws_o + (slot * p.rows_cap + r) * D + 32 * cc);
+                uint4* dst = reinterpret_cast<uint4*>(p.ws_o + (slot * p.rows_cap + r) * p.ws_pitch + 32 * cc);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
               }

@@ -400,7 +400,7 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
                 for (int e = 0; e < E / 2; ++e) op[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
                 if (lane == 0) p.lse[row] = paged_lse(mm, ll);
               } else {
-                float* op = p.ws_o + (slot * p.rows_cap + r) * D + lane * E;
+                float* op = p.ws_o + (slot * p.rows_cap + r) * p.ws_pitch + lane * E;
 #pragma unroll
                 for (int e = 0; e < E; ++e) op[e] = acc[e];
                 if (lane == 0) p.ws_ml[slot * p.rows_cap + r] = make_float2(mm, ll);

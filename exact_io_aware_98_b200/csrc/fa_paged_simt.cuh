@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(128) fa_paged_simt_kernel(const PagedParams p)
             if (lane * 4 + c < d) op[lane * 4 + c] = from_f<T>(ov[c] * inv);
           if (lane == 0) p.lse[row] = paged_lse(mm, ll);
         } else {
-          float* op = p.ws_o + (slot * p.rows_cap + r) * d;
+          float* op = p.ws_o + (slot * p.rows_cap + r) * p.ws_pitch;
           const float ov[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
