@@ -8,6 +8,7 @@ library is missing or no GPU is present, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple, Optional
@@ -264,36 +265,42 @@ def bwd_noalloc(q, k, v, o, lse, do, scale: Optional[float] = None, causal: bool
 ROPE_INTERLEAVED, ROPE_BACKWARD = 1, 2   # fa.h FA_ROPE_*
 
 
-def _on(device, t, name: str, dtype=None):
-    """Checks that t is on ``device`` (a CUDA device) with ``dtype``; no contiguity asked."""
-    if not t.is_cuda:
-        raise FaError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise FaError(f"{name} is on {t.device}, not {device}")
-    if dtype is not None and t.dtype != dtype:
-        raise FaError(f"{name} must be {dtype}, got {t.dtype}")
+# The calls below are a few microseconds of GPU work at a decoding step's sizes, so their checks are
+# written for the host: device numbers, shapes and dtypes are compared directly, and only a
+# comparison that fails goes through the functions that say which.
 
 
-def _flat(device, t, name: str, dtype, shape=None):
-    """_on for a contiguous tensor, of ``shape`` when given."""
-    _on(device, t, name, dtype)
-    if not t.is_contiguous():
-        raise FaError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape:
-        raise FaError(f"{name} shape {tuple(t.shape)} must be {tuple(shape)}")
+def _refuse(dev: int, *specs):
+    """Raises for the first (name, tensor, dtype, shape or None, contiguous) that does not hold on
+    CUDA device ``dev``; returns if all do."""
+    for name, t, dtype, shape, contiguous in specs:
+        if not t.is_cuda:
+            raise FaError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise FaError(f"{name} is on {t.device}, not cuda:{dev}")
+        if dtype is not None and t.dtype is not dtype:
+            raise FaError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise FaError(f"{name} shape {tuple(t.shape)} must be {tuple(shape)}")
+        if contiguous and not t.is_contiguous():
+            raise FaError(f"{name} must be contiguous")
 
 
-def _call(device, name: str, *args):
-    """One library call on ``device``'s current stream, whatever device is current."""
-    fn = getattr(load(), name)
-    index = device.index
-    if index == torch.cuda.current_device():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_strides3 = functools.lru_cache(maxsize=4096)(lambda *x: (_l * 3)(*x))
+_strides8 = functools.lru_cache(maxsize=4096)(lambda *x: (_l * 8)(*x))
+
+
+def _call(dev: int, fn, *args):
+    """One library call on CUDA device ``dev``'s current stream, whatever device is current."""
+    if dev == _get_device():
+        rc = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(index):
-            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
     if rc != 0:
-        _check(rc, name)
+        _check(rc, fn.__name__)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
@@ -331,39 +338,43 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[s
     return f.to(device), magnitude
 
 
-def _rope(x, inv_freq, positions, interleaved, magnitude, out, backward):
-    dev = x.device
-    _on(dev, x, "x")
-    _flat(dev, inv_freq, "inv_freq", torch.float64)
-    packed = x.dim() == 3
-    if not packed and x.dim() != 4:
-        raise FaError(f"x must be [B, H, N, d] or [T, H, d], got {tuple(x.shape)}")
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-    if out is not None:
-        _on(dev, y, "out", x.dtype)
-        if y.shape != x.shape:
-            raise FaError(f"out shape {tuple(y.shape)} must be {tuple(x.shape)}")
-    d = x.shape[-1]
-    if d > 1 and (x.stride(-1) != 1 or y.stride(-1) != 1):
-        raise FaError("the last dimension of x and out must be contiguous")
-    xs, ys = x.stride(), y.stride()
-    if packed:
-        (N, H), B = x.shape[:2], 1
-        xs, ys = (0, xs[1], xs[0]), (0, ys[1], ys[0])
+def _rope(x, inv_freq, positions, interleaved, magnitude, out, options):
+    lib = _lib or load()
+    dev = x.get_device()
+    dtype, shape, xs = x.dtype, x.shape, x.stride()
+    y = out
+    if y is None:
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+    ys = y.stride()
+    if dev < 0 or dev != inv_freq.get_device() or dev != y.get_device() or y.dtype is not dtype or \
+            inv_freq.dtype is not torch.float64 or not inv_freq.is_contiguous() or y.shape != shape:
+        _refuse(dev, ("x", x, None, None, False), ("inv_freq", inv_freq, torch.float64, None, True),
+                ("out", y, dtype, shape, False))
+    if len(shape) == 3:
+        N, H, d = shape
+        B = 1
+        xa, ya = _strides3(0, xs[1], xs[0]), _strides3(0, ys[1], ys[0])
+    elif len(shape) == 4:
+        B, H, N, d = shape
+        xa, ya = _strides3(*xs[:3]), _strides3(*ys[:3])
     else:
-        B, H, N = x.shape[:3]
-    ps = 0
+        raise FaError(f"x must be [B, H, N, d] or [T, H, d], got {tuple(shape)}")
+    if d > 1 and (xs[-1] != 1 or ys[-1] != 1):
+        raise FaError("the last dimension of x and out must be contiguous")
+    ps, pp = 0, None
     if positions is not None:
-        _on(dev, positions, "positions", torch.int32)
-        if positions.shape != (N,) and (packed or positions.shape != (B, N)):
-            raise FaError(f"positions shape {tuple(positions.shape)} does not match x {tuple(x.shape)}")
+        if positions.get_device() != dev or positions.dtype is not torch.int32:
+            _refuse(dev, ("positions", positions, torch.int32, None, False))
+        if positions.shape != (N,):
+            if len(shape) == 3 or positions.shape != (B, N):
+                raise FaError(f"positions shape {tuple(positions.shape)} does not match x {tuple(shape)}")
+            ps = positions.stride(0)
         if N > 1 and positions.stride(-1) != 1:
             raise FaError("positions must be contiguous along the tokens")
-        ps = positions.stride(0) if positions.dim() == 2 else 0
-    _call(dev, "fa_rope", x.data_ptr(), y.data_ptr(), _ptr(positions), inv_freq.data_ptr(), B, H, N,
-          d, 2 * inv_freq.numel(), (_l * 3)(*xs[:3]), (_l * 3)(*ys[:3]), ps, float(magnitude),
-          (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_BACKWARD if backward else 0),
-          _dtype_code(x))
+        pp = positions.data_ptr()
+    _call(dev, lib.fa_rope, x.data_ptr(), y.data_ptr(), pp, inv_freq.data_ptr(), B, H, N, d,
+          2 * inv_freq.numel(), xa, ya, ps, float(magnitude),
+          options | ROPE_INTERLEAVED if interleaved else options, _dtype_code(x))
     return y
 
 
@@ -371,13 +382,13 @@ def rope(x, inv_freq, positions=None, interleaved: bool = False, magnitude: floa
     """Rotary positions (fa_rope) on x [B, H, N, d] or packed [T, H, d], bf16 or fp32, any
     strides with d contiguous; the first 2 * len(inv_freq) columns turn.  positions int32 [N]
     or [B, N] ([T] when packed), default 0 .. N-1.  ``out`` may be x."""
-    return _rope(x, inv_freq, positions, interleaved, magnitude, out, False)
+    return _rope(x, inv_freq, positions, interleaved, magnitude, out, 0)
 
 
 def rope_bwd(dy, inv_freq, positions=None, interleaved: bool = False, magnitude: float = 1.0,
              out=None):
     """dL/dx of ``rope`` from dL/dy, with the same arguments."""
-    return _rope(dy, inv_freq, positions, interleaved, magnitude, out, True)
+    return _rope(dy, inv_freq, positions, interleaved, magnitude, out, ROPE_BACKWARD)
 
 
 class PagedPlan(NamedTuple):
@@ -400,48 +411,63 @@ def paged_plan(ctx_len, new_len, free_pages, block_table, page_size: int, max_to
     """One step's bookkeeping on the GPU (fa_paged_plan): ctx_len and new_len int32 [B],
     free_pages int32 [F] (handed out from ``cursor``, int32 [1], on), block_table int32
     [B, max_pages] updated in place.  ``out`` reuses an earlier plan's tensors."""
-    dev = ctx_len.device
+    lib = _lib or load()
+    dev = ctx_len.get_device()
     B = ctx_len.numel()
-    _flat(dev, ctx_len, "ctx_len", torch.int32, (B,))
-    _flat(dev, new_len, "new_len", torch.int32, (B,))
-    _flat(dev, free_pages, "free_pages", torch.int32)
-    _on(dev, block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B or block_table.shape[1] < 1 or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise FaError(f"block_table must be [{B}, max_pages] with contiguous rows")
-    if cursor is not None:
-        _flat(dev, cursor, "cursor", torch.int32)
-        if cursor.numel() != 1:
-            raise FaError("cursor must hold one number")
     max_tokens = int(max_tokens)
     if out is None:
         if max_tokens < 1 or B < 1:
             raise FaError("paged_plan needs at least one request and max_tokens >= 1")
-        out = PagedPlan.empty(B, max_tokens, dev)
-    else:
-        for t, n, dt, size in ((out.cu_q, "cu_q", torch.int32, B + 1), (out.kv_len, "kv_len", torch.int32, B),
-                               (out.positions, "positions", torch.int32, max_tokens),
-                               (out.slots, "slots", torch.int64, max_tokens),
-                               (out.counts, "counts", torch.int32, 4)):
-            _flat(dev, t, n, dt, (size,))
-    _call(dev, "fa_paged_plan", ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
-          free_pages.numel(), _ptr(cursor), block_table.data_ptr(), block_table.stride(0), B,
-          block_table.shape[1], int(page_size), max_tokens, out.cu_q.data_ptr(),
-          out.kv_len.data_ptr(), out.positions.data_ptr(), out.slots.data_ptr(),
-          out.counts.data_ptr())
+        out = PagedPlan.empty(B, max_tokens, ctx_len.device)
+    cu_q, kv_len, positions, slots, counts = out
+    i32 = torch.int32
+    if not (dev >= 0 and dev == new_len.get_device() == free_pages.get_device() == block_table.get_device()
+            == cu_q.get_device() == kv_len.get_device() == positions.get_device() == slots.get_device()
+            == counts.get_device()
+            and ctx_len.dtype is i32 and new_len.dtype is i32 and free_pages.dtype is i32
+            and block_table.dtype is i32 and cu_q.dtype is i32 and kv_len.dtype is i32
+            and positions.dtype is i32 and slots.dtype is torch.int64 and counts.dtype is i32
+            and ctx_len.is_contiguous() and new_len.is_contiguous() and free_pages.is_contiguous()
+            and cu_q.is_contiguous() and kv_len.is_contiguous() and positions.is_contiguous()
+            and slots.is_contiguous() and counts.is_contiguous()
+            and ctx_len.dim() == 1 and new_len.shape == (B,) and cu_q.shape == (B + 1,) and kv_len.shape == (B,)
+            and positions.shape == (max_tokens,) and slots.shape == (max_tokens,) and counts.shape == (4,)):
+        _refuse(dev, ("ctx_len", ctx_len, i32, (B,), True), ("new_len", new_len, i32, (B,), True),
+                ("free_pages", free_pages, i32, None, True), ("block_table", block_table, i32, None, False),
+                ("cu_q", cu_q, i32, (B + 1,), True), ("kv_len", kv_len, i32, (B,), True),
+                ("positions", positions, i32, (max_tokens,), True),
+                ("slots", slots, torch.int64, (max_tokens,), True), ("counts", counts, i32, (4,), True))
+    ts, stride = block_table.shape, block_table.stride()
+    if len(ts) != 2 or ts[0] != B or ts[1] < 1 or (ts[1] > 1 and stride[1] != 1):
+        raise FaError(f"block_table must be [{B}, max_pages] with contiguous rows")
+    cp = None
+    if cursor is not None:
+        _refuse(dev, ("cursor", cursor, i32, None, True))
+        if cursor.numel() != 1:
+            raise FaError("cursor must hold one number")
+        cp = cursor.data_ptr()
+    _call(dev, lib.fa_paged_plan, ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
+          free_pages.numel(), cp, block_table.data_ptr(), stride[0], B, ts[1], int(page_size), max_tokens,
+          cu_q.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), slots.data_ptr(), counts.data_ptr())
     return out
 
 
-def _cache(dev, k_cache, v_cache, dtype, H_kv: int, d: int):
-    """Checks of a paged cache pair [num_pages, H_kv, page_size, d]; (num_pages, page_size)."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _on(dev, t, n, dtype)
-        if t.dim() != 4 or t.shape[1] != H_kv or t.shape[3] != d or t.shape != k_cache.shape:
-            raise FaError(f"{n} shape {tuple(t.shape)} must be [pages, {H_kv}, page_size, {d}]")
-        page = t.shape[2]
-        if t.stride(3) != 1 or t.stride(2) != d or (H_kv > 1 and t.stride(1) != page * d):
-            raise FaError(f"each page of {n} must be contiguous")
-    return k_cache.shape[0], k_cache.shape[2]
+def _cache(dev: int, k_cache, v_cache, dtype, H_kv: int, d: int):
+    """Checks of a paged cache pair [num_pages, H_kv, page_size, d]; (num_pages, page_size and the
+    page strides)."""
+    shape, ks, vs = k_cache.shape, k_cache.stride(), v_cache.stride()
+    if k_cache.get_device() != dev or v_cache.get_device() != dev or k_cache.dtype is not dtype or \
+            v_cache.dtype is not dtype or v_cache.shape != shape:
+        _refuse(dev, ("k_cache", k_cache, dtype, None, False), ("v_cache", v_cache, dtype, shape, False))
+    if len(shape) != 4 or shape[1] != H_kv or shape[3] != d:
+        raise FaError(f"k_cache shape {tuple(shape)} must be [pages, {H_kv}, page_size, {d}]")
+    page = shape[2]
+    inner = (page * d, d, 1)
+    if ks[1:] != inner or vs[1:] != inner:
+        for n, st in (("k_cache", ks), ("v_cache", vs)):
+            if st[3] != 1 or st[2] != d or (H_kv > 1 and st[1] != page * d):
+                raise FaError(f"each page of {n} must be contiguous")
+    return shape[0], page, ks[0], vs[0]
 
 
 def paged_append(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None,
@@ -450,46 +476,48 @@ def paged_append(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None,
     page_size, d] (fa_paged_append); with inv_freq and positions (int32 [T]) the keys are rotated
     as ``rope`` does.  q [T, H, d] is rotated alongside into q_out (allocated when None; may be
     q), which is returned (None without q)."""
-    dev = k.device
-    _on(dev, k, "k")
-    _on(dev, v, "v", k.dtype)
-    if k.dim() != 3 or v.shape != k.shape:
-        raise FaError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must both be [T, H_kv, d]")
-    T, H_kv, d = k.shape
-    pages, page = _cache(dev, k_cache, v_cache, k.dtype, H_kv, d)
-    _flat(dev, slots, "slots", torch.int64, (T,))
-    rot = 0
+    lib = _lib or load()
+    dev = k.get_device()
+    dtype, shape = k.dtype, k.shape
+    if dev < 0 or v.get_device() != dev or v.dtype is not dtype or v.shape != shape or \
+            slots.get_device() != dev or slots.dtype is not torch.int64 or slots.shape != shape[:1] or \
+            not slots.is_contiguous():
+        _refuse(dev, ("k", k, None, None, False), ("v", v, dtype, shape, False),
+                ("slots", slots, torch.int64, shape[:1], True))
+    if len(shape) != 3:
+        raise FaError(f"k {tuple(shape)} and v must both be [T, H_kv, d]")
+    T, H_kv, d = shape
+    pages, page, k_page, v_page = _cache(dev, k_cache, v_cache, dtype, H_kv, d)
+    rot, pp, fp = 0, None, None
     if inv_freq is not None:
-        _flat(dev, inv_freq, "inv_freq", torch.float64)
         if positions is None:
             raise FaError("inv_freq needs positions")
-        _flat(dev, positions, "positions", torch.int32, (T,))
-        rot = 2 * inv_freq.numel()
-    H = 0
-    qs = qos = (0, 0, 1)
+        if inv_freq.get_device() != dev or positions.get_device() != dev or \
+                inv_freq.dtype is not torch.float64 or positions.dtype is not torch.int32 or \
+                positions.shape != (T,) or not inv_freq.is_contiguous() or not positions.is_contiguous():
+            _refuse(dev, ("inv_freq", inv_freq, torch.float64, None, True),
+                    ("positions", positions, torch.int32, (T,), True))
+        rot, pp, fp = 2 * inv_freq.numel(), positions.data_ptr(), inv_freq.data_ptr()
+    ks, vs = k.stride(), v.stride()
+    H, qp, qop, qs, qos = 0, None, None, (0, 0, 1), (0, 0, 1)
     if q is not None:
-        _on(dev, q, "q", k.dtype)
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d:
-            raise FaError(f"q shape {tuple(q.shape)} must be [{T}, H, {d}]")
-        H = q.shape[1]
+        qshape = q.shape
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        else:
-            _on(dev, q_out, "q_out", q.dtype)
-            if q_out.shape != q.shape:
-                raise FaError(f"q_out shape {tuple(q_out.shape)} must be {tuple(q.shape)}")
-        qs, qos = q.stride(), q_out.stride()
+            q_out = torch.empty(qshape, dtype=q.dtype, device=q.device)
+        if q.get_device() != dev or q_out.get_device() != dev or q.dtype is not dtype or \
+                q_out.dtype is not dtype or q_out.shape != qshape:
+            _refuse(dev, ("q", q, dtype, None, False), ("q_out", q_out, dtype, qshape, False))
+        if len(qshape) != 3 or qshape[0] != T or qshape[2] != d:
+            raise FaError(f"q shape {tuple(qshape)} must be [{T}, H, {d}]")
+        H, qp, qop, qs, qos = qshape[1], q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
     elif q_out is not None:
         raise FaError("q_out without q")
-    ks, vs = k.stride(), v.stride()
     if d > 1 and (qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or qos[2] != 1):
         raise FaError("the last dimension of q, k, v and q_out must be contiguous")
-    _call(dev, "fa_paged_append", _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out),
-          k_cache.data_ptr(), v_cache.data_ptr(), slots.data_ptr(),
-          None if rot == 0 else positions.data_ptr(), _ptr(inv_freq), T, H, H_kv, d, rot,
-          (_l * 8)(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qos[0], qos[1]), k_cache.stride(0),
-          v_cache.stride(0), page, pages, float(magnitude), ROPE_INTERLEAVED if interleaved else 0,
-          _dtype_code(k))
+    _call(dev, lib.fa_paged_append, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
+          v_cache.data_ptr(), slots.data_ptr(), pp, fp, T, H, H_kv, d, rot,
+          _strides8(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qos[0], qos[1]), k_page, v_page, page,
+          pages, float(magnitude), ROPE_INTERLEAVED if interleaved else 0, _dtype_code(k))
     return q_out
 
 
@@ -504,43 +532,46 @@ def paged_fwd(q, k_cache, v_cache, block_table, kv_len, cu_q, scale: Optional[fl
     [B, max_pages], kv_len int32 [B], cu_q int32 [B + 1].  O is [T, H, d], lse [T, H]; rows that
     no request owns are not written.  ``max_q``, the most new tokens of any request, helps to
     choose the kernel."""
-    dev = q.device
-    _on(dev, q, "q")
-    if q.dim() != 3:
-        raise FaError(f"q must be [T, H, d], got {tuple(q.shape)}")
-    T, H, d = q.shape
-    if d > 1 and q.stride(2) != 1:
+    lib = _lib or load()
+    dev = q.get_device()
+    dtype, shape, qs, ts, stride = q.dtype, q.shape, q.stride(), block_table.shape, block_table.stride()
+    if dev < 0:
+        _refuse(dev, ("q", q, None, None, False))
+    if len(shape) != 3:
+        raise FaError(f"q must be [T, H, d], got {tuple(shape)}")
+    T, H, d = shape
+    if d > 1 and qs[2] != 1:
         raise FaError("the last dimension of q must be contiguous")
     if k_cache.dim() != 4:
         raise FaError("k_cache must be [pages, H_kv, page_size, d]")
     H_kv = k_cache.shape[1]
-    pages, page = _cache(dev, k_cache, v_cache, q.dtype, H_kv, d)
+    pages, page, k_page, v_page = _cache(dev, k_cache, v_cache, dtype, H_kv, d)
     B = kv_len.numel()
-    _flat(dev, kv_len, "kv_len", torch.int32, (B,))
-    _flat(dev, cu_q, "cu_q", torch.int32, (B + 1,))
-    _on(dev, block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    if len(ts) != 2 or ts[0] != B or (ts[1] > 1 and stride[1] != 1):
         raise FaError(f"block_table must be [{B}, max_pages] with contiguous rows")
     if out is None:
-        out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
-    else:
-        _flat(dev, out, "out", q.dtype, q.shape)
+        out = torch.empty((T, H, d), dtype=dtype, device=q.device)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    else:
-        _flat(dev, lse, "lse", torch.float32, (T, H))
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(paged_workspace_size(T, B, H, H_kv, d), dtype=torch.uint8, device=dev)
-    else:
-        _flat(dev, workspace, "workspace", torch.uint8)
-    qs = q.stride()
-    _call(dev, "fa_paged_fwd", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        workspace = torch.empty(paged_workspace_size(T, B, H, H_kv, d), dtype=torch.uint8, device=q.device)
+    i32 = torch.int32
+    if not (dev == kv_len.get_device() == cu_q.get_device() == block_table.get_device() == out.get_device()
+            == lse.get_device() == workspace.get_device()
+            and kv_len.dtype is i32 and cu_q.dtype is i32 and block_table.dtype is i32 and out.dtype is dtype
+            and lse.dtype is torch.float32 and workspace.dtype is torch.uint8
+            and kv_len.dim() == 1 and cu_q.shape == (B + 1,) and out.shape == shape and lse.shape == shape[:2]
+            and kv_len.is_contiguous() and cu_q.is_contiguous() and out.is_contiguous()
+            and lse.is_contiguous() and workspace.is_contiguous()):
+        _refuse(dev, ("kv_len", kv_len, i32, (B,), True), ("cu_q", cu_q, i32, (B + 1,), True),
+                ("block_table", block_table, i32, None, False), ("out", out, dtype, shape, True),
+                ("lse", lse, torch.float32, shape[:2], True), ("workspace", workspace, torch.uint8, None, True))
+    _call(dev, lib.fa_paged_fwd, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           block_table.data_ptr(), kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          T, B, H, H_kv, d, qs[0], qs[1], k_cache.stride(0), v_cache.stride(0),
-          block_table.stride(0), page, pages, block_table.shape[1],
+          T, B, H, H_kv, d, qs[0], qs[1], k_page, v_page, stride[0], page, pages, ts[1],
           0 if max_q is None else int(max_q), default_scale(d) if scale is None else float(scale),
-          int(causal), _dtype_code(q), workspace.data_ptr(), workspace.numel())
+          1 if causal else 0,
+          _dtype_code(q), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
