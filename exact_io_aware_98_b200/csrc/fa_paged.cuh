@@ -10,12 +10,15 @@
 // ("tile head": H_kv * splits of them).
 //
 // The division.  An item is one (row tile, K/V head); its cost is the number n of key tiles its
-// rows can see (at least 1, so that a row with no key gets its O = 0 and lse = -inf).  The items
-// of the batch laid end to end form a line of W key tiles, which is cut into equal shares, one
-// per CTA.  So a batch of any mix of lengths loads all SMs alike, a single long request is
+// rows can see (at least 1, so that a row with no key gets its O = 0 and lse = -inf) plus a
+// constant for its start and its output, in units of a tile (the kernels measure it: without it,
+// the CTA that gets the short items of a causal prompt's beginning finished last, at twice the
+// time of the others).  The items of the batch laid end to end form a line of length W, which is
+// cut into equal shares, one per CTA; an item's constant lies behind its tiles, so a cut there
+// leaves the item whole.  So a batch of any mix of lengths loads all SMs alike, a single long request is
 // spread over all of them, and every CTA has at most one item that it continues for the CTA
 // before it and at most one that it leaves unfinished.  Those two pieces go to the workspace as
-// unnormalised fp32 sums with their row maximum and row sum; fa_paged_join_kernel adds them in
+// unnormalised fp32 sums with their row maximum and row sum; fa_paged_join kernels adds them in
 // the order of the keys.  Every other item is finished where it was computed.  The division
 // depends on the lengths only, so results do not vary between runs.  Each CTA computes it from
 // the lengths on its own: no host copy of the lengths, no extra launch, and a captured call
@@ -42,7 +45,8 @@ struct PagedParams {
   int group;                   // query heads per K/V head
   int G, splits;               // heads per tile, tiles per group (ceil(group / G))
   int Hv;                      // tile heads: H_kv * splits
-  int vec;                     // rows and strides allow 16-byte copies
+  int vec;                     // cache rows and strides allow 16-byte copies
+  int o_al32;                  // o is 32-byte aligned
   int page_shift, num_pages, max_pages;
   int causal;
   float scale2;                // scale * log2(e)
@@ -69,7 +73,8 @@ struct PagedSched {
   long long tmp[33];
   PagedRec rec[PAGED_RECS];
   int n_rec;
-  long long stop;  // end of the listed part of the CTA's share
+  long long stop;        // end of the listed part of the CTA's share
+  long long W, ctas;     // the line's length, the CTAs that share it
 };
 
 // Row r of a tile of tile head h: its token within the tile and its query head (-1: the tile has
@@ -81,57 +86,80 @@ __device__ __forceinline__ int paged_row_head(const PagedParams& p, int h, int r
 }
 
 struct PagedReq {
-  int tok0, nq, kv, tiles_per;  // tiles_per: tokens per row tile
+  int tok0, nq, kv;
 };
 
-__device__ __forceinline__ PagedReq paged_req(const PagedParams& p, int b, int tpt) {
+__device__ __forceinline__ PagedReq paged_req(const PagedParams& p, int b) {
   PagedReq r;
   const int lo = min(max(p.cu_q[b], 0), p.T), hi = min(max(p.cu_q[b + 1], 0), p.T);
-  const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
   r.tok0 = lo;
   r.nq = max(hi - lo, 0);
-  r.kv = static_cast<int>(min(static_cast<long long>(max(p.kv_len[b], 0)), room));
-  r.tiles_per = tpt;
+  r.kv = min(max(p.kv_len[b], 0), p.max_pages << p.page_shift);  // at most 2^30
   return r;
 }
 
-// Keys that the tokens [t tpt, t tpt + ntok) of a request can see between them.
+// Keys that a tile's tokens can see between them, the first at position pos0.
 __device__ __forceinline__ int paged_keys(int causal, int kv, int pos0, int ntok) {
-  if (!causal) return kv;
-  const long long last = static_cast<long long>(pos0) + ntok;  // one past the last token
-  return static_cast<int>(min(max(last, 0ll), static_cast<long long>(kv)));
+  return causal ? min(max(pos0 + ntok, 0), kv) : kv;
 }
 
-// Key tiles of row tile t (KT keys each, at least one).
+// Key tiles (of KT keys, at least one) of row tile t of a request.
 template <int KT>
-__device__ __forceinline__ int paged_tiles(int causal, const PagedReq& r, int t) {
-  const int ntok = min(r.tiles_per, r.nq - t * r.tiles_per);
-  const int keys = paged_keys(causal, r.kv, r.kv - r.nq + t * r.tiles_per, ntok);
-  return max(1, (keys + KT - 1) / KT);
+__device__ __forceinline__ int paged_tiles(int causal, const PagedReq& r, int tpt, int t) {
+  const int keys = causal ? r.kv - r.nq + min(r.nq, (t + 1) * tpt) : r.kv;
+  return (max(keys, 1) + KT - 1) / KT;
 }
 
-// Key tiles of all row tiles of a request, for one K/V head.
-template <int KT>
-__device__ __forceinline__ long long paged_cost(const PagedParams& p, const PagedReq& r) {
-  const int nt = (r.nq + r.tiles_per - 1) / r.tiles_per;
-  if (!p.causal) return static_cast<long long>(nt) * max(1, (r.kv + KT - 1) / KT);
-  long long c = 0;
-  for (int t = 0; t < nt; ++t) c += paged_tiles<KT>(1, r, t);
-  return c;
+// sum of (a j + b) / m (rounded down) over j in [0, n), a, b >= 0: the Euclidean recursion, two
+// rounds where a divides m or m divides a.  a n + b fits 32 bits.
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long s = 0;
+  while (n > 0) {
+    s += static_cast<long long>(n) * (n - 1) / 2 * (a / m) + static_cast<long long>(n) * (b / m);
+    a %= m;
+    b %= m;
+    const unsigned y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const unsigned t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// Length of the first t row tiles of a request for one tile head (t at most their number); C: an
+// item's constant.  In closed form: a prompt has thousands of row tiles.
+template <int KT, int C>
+__device__ __forceinline__ long long paged_prefix(int causal, const PagedReq& r, int tpt, int t) {
+  const long long each = static_cast<long long>(t) * C;
+  if (!causal) return each + static_cast<long long>(t) * ((max(r.kv, 1) + KT - 1) / KT);
+  const int base = r.kv - r.nq;  // keys before the request's tokens (negative: rows without keys)
+  const int full = min(t, r.nq / tpt);                       // tiles of tpt tokens
+  const int none = base < 0 ? min(full, -base / tpt) : 0;    // whose rows see no key: one key tile
+  long long s = each + none;
+  if (full > none)
+    s += floor_sum(full - none, KT, tpt, base + (none + 1) * tpt + KT - 1);
+  if (t > full) s += (max(r.kv, 1) + KT - 1) / KT;           // the last, shorter tile
+  return s;
 }
 
 // The length W of the line.  Every thread of the block (NT) calls it.
-template <int KT, int NT>
+template <int KT, int C, int NT>
 __device__ long long paged_total(const PagedParams& p, int tpt, PagedSched& s) {
   long long mine = 0, all;
-  for (int b = threadIdx.x; b < p.B; b += NT) mine += paged_cost<KT>(p, paged_req(p, b, tpt));
+  for (int b = threadIdx.x; b < p.B; b += NT) {
+    const PagedReq r = paged_req(p, b);
+    mine += paged_prefix<KT, C>(p.causal, r, tpt, (r.nq + tpt - 1) / tpt);
+  }
   block_excl_scan<long long, NT>(mine, s.tmp, &all);
   return all * p.Hv;
 }
 
 // Lists the row tiles that [lo, hi) of the line touches, PAGED_RECS at most, and sets s.stop to
 // where the listed part ends.  Every thread of the block calls it, lo < hi.
-template <int KT, int NT>
+template <int KT, int C, int NT>
 __device__ void paged_list(const PagedParams& p, int tpt, long long lo, long long hi,
                            PagedSched& s) {
   if (threadIdx.x == 0) s.stop = hi;
@@ -139,90 +167,124 @@ __device__ void paged_list(const PagedParams& p, int tpt, long long lo, long lon
   int listed = 0;
   for (int b0 = 0; b0 < p.B && carry < hi && listed < PAGED_RECS; b0 += NT) {
     const int b = b0 + static_cast<int>(threadIdx.x);
-    PagedReq r = {0, 0, 0, 1};
-    if (b < p.B) r = paged_req(p, b, tpt);
-    long long sum, lin = 0;
-    const long long cost = b < p.B ? paged_cost<KT>(p, r) * p.Hv : 0;
-    lin = carry + block_excl_scan<long long, NT>(cost, s.tmp, &sum);
-    const int nt = (r.nq + r.tiles_per - 1) / r.tiles_per;
-    int count = 0;
-    const bool touch = cost > 0 && lin < hi && lin + cost > lo;
-    if (touch) {
-      long long x = lin;
-      for (int t = 0; t < nt && x < hi; ++t) {
-        const long long e = x + static_cast<long long>(paged_tiles<KT>(p.causal, r, t)) * p.Hv;
-        if (e > lo) ++count;
-        x = e;
-      }
-    }
-    long long all;
-    long long at = listed + block_excl_scan<long long, NT>(count, s.tmp, &all);
-    if (count > 0 && at < PAGED_RECS) {
-      long long x = lin;
-      for (int t = 0; t < nt && x < hi && at < PAGED_RECS; ++t) {
-        const int n = paged_tiles<KT>(p.causal, r, t);
-        const long long e = x + static_cast<long long>(n) * p.Hv;
-        if (e > lo) {
-          PagedRec c;
-          c.lin = x;
-          c.b = b;
-          c.tok0 = r.tok0 + t * r.tiles_per;
-          c.ntok = min(r.tiles_per, r.nq - t * r.tiles_per);
-          c.pos0 = r.kv - r.nq + t * r.tiles_per;
-          c.kv = r.kv;
-          c.n = n;
-          s.rec[at] = c;
-          if (at == PAGED_RECS - 1) s.stop = min(hi, e);
-          ++at;
+    PagedReq r = {0, 0, 0};
+    if (b < p.B) r = paged_req(p, b);
+    const int nt = (r.nq + tpt - 1) / tpt;
+    const long long cost = paged_prefix<KT, C>(p.causal, r, tpt, nt) * p.Hv;
+    long long sum;
+    const long long lin = carry + block_excl_scan<long long, NT>(cost, s.tmp, &sum);
+    // this request's first row tile that ends behind lo, where it starts, and how many from it
+    // on (PAGED_RECS at most) start before hi
+    int t0 = 0, count = 0;
+    long long x0 = lin;
+    if (cost > 0 && lin < hi && lin + cost > lo) {
+      if (lin < lo) {
+        int end = nt;  // the tile is in [t0, end)
+        while (end - t0 > 1) {
+          const int mid = (t0 + end) >> 1;
+          if (lin + paged_prefix<KT, C>(p.causal, r, tpt, mid) * p.Hv <= lo) t0 = mid; else end = mid;
         }
-        x = e;
+        x0 = lin + paged_prefix<KT, C>(p.causal, r, tpt, t0) * p.Hv;
       }
+      long long x = x0;
+      for (int t = t0; t < nt && x < hi && count < PAGED_RECS; ++t, ++count)
+        x += static_cast<long long>(paged_tiles<KT>(p.causal, r, tpt, t) + C) * p.Hv;
+    }
+    int all;
+    int at = listed + block_excl_scan<int, NT>(count, reinterpret_cast<int*>(s.tmp), &all);
+    for (int t = t0; t < t0 + count && at < PAGED_RECS; ++t, ++at) {
+      PagedRec c;
+      c.lin = x0;
+      c.b = b;
+      c.tok0 = r.tok0 + t * tpt;
+      c.ntok = min(tpt, r.nq - t * tpt);
+      c.pos0 = r.kv - r.nq + t * tpt;
+      c.kv = r.kv;
+      c.n = paged_tiles<KT>(p.causal, r, tpt, t);
+      s.rec[at] = c;
+      x0 += static_cast<long long>(c.n + C) * p.Hv;
+      if (at == PAGED_RECS - 1) s.stop = min(hi, x0);
     }
     carry += sum;
-    listed = static_cast<int>(min(listed + all, static_cast<long long>(PAGED_RECS)));
+    listed = min(listed + all, PAGED_RECS);
   }
   if (threadIdx.x == 0) s.n_rec = listed;
   __syncthreads();
 }
 
-// One piece: key tiles [a, b) of the item (record, tile head h).
+// One piece: key tiles [a, b) of the item (record, tile head h), a < b.
 struct PagedPiece {
   int rec, h, a, b;
-  long long item_end;  // end of the whole item on the line
 };
 
-// The piece that starts at x of the line; `rec` is where the search starts (records are in
-// order and x only grows).
-__device__ __forceinline__ PagedPiece paged_piece(const PagedParams& p, const PagedSched& s,
-                                                  long long x, int rec) {
-  while (rec + 1 < s.n_rec && x >= s.rec[rec + 1].lin) ++rec;
-  PagedPiece c;
-  const int n = s.rec[rec].n;
-  const long long off = x - s.rec[rec].lin;
-  c.rec = rec;
-  c.h = static_cast<int>(off / n);
-  c.a = static_cast<int>(off - static_cast<long long>(c.h) * n);
-  c.b = static_cast<int>(min(static_cast<long long>(n), c.a + (s.stop - x)));
-  c.item_end = s.rec[rec].lin + static_cast<long long>(c.h + 1) * n;
-  return c;
-}
-
-// The share of CTA c of `ctas` on a line of W >= ctas tiles.
-__device__ __forceinline__ long long paged_cut(long long W, long long c, long long ctas) {
-  return W * c / ctas;
-}
+// Walks over the pieces of the listed part of a CTA's share.
+template <int C>
+struct PagedPieces {
+  long long x;  // where the next piece is looked for
+  int rec, h, off;  // its item, and how far x is into it
+  __device__ __forceinline__ void start(const PagedParams&, const PagedSched& s, long long x0) {
+    x = x0;
+    rec = 0;
+    while (rec + 1 < s.n_rec && x >= s.rec[rec + 1].lin) ++rec;
+    const int len = s.rec[rec].n + C;
+    const long long d = x - s.rec[rec].lin;
+    h = static_cast<int>(d / len);
+    off = static_cast<int>(d - static_cast<long long>(h) * len);
+  }
+  __device__ __forceinline__ bool next(const PagedParams& p, const PagedSched& s, PagedPiece& c) {
+    while (x < s.stop) {
+      const int n = s.rec[rec].n;
+      const int step = static_cast<int>(min(static_cast<long long>(n + C - off), s.stop - x));
+      c.rec = rec;
+      c.h = h;
+      c.a = off;
+      c.b = min(n, off + step);
+      const bool some = off < n;
+      x += step;
+      off = 0;
+      if (++h == p.Hv) {
+        h = 0;
+        ++rec;
+      }
+      if (some) return true;
+    }
+    return false;
+  }
+};
 
 // Where a piece's partial sums go: slot 0 continues an item, slot 1 leaves one unfinished.
 __device__ __forceinline__ size_t paged_slot(int cta, const PagedPiece& c) {
   return static_cast<size_t>(cta) * 2 + (c.a > 0 ? 0 : 1);
 }
 
+// Start of a CTA: its share [lo, hi) of the line, and an empty header.  false: nothing to do.
+// Every thread of the block calls it.
+template <int KT, int C, int NT>
+__device__ __forceinline__ bool paged_share(const PagedParams& p, int tpt, PagedSched& s, long long& lo,
+                                            long long& hi) {
+  const long long W = paged_total<KT, C, NT>(p, tpt, s);
+  const long long ctas = min(static_cast<long long>(gridDim.x), W);
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    s.W = W;
+    s.ctas = ctas;
+    p.ws_head[cta] = make_int4(0, 0, 0, 0);
+  }
+  if (cta >= ctas) return false;
+  lo = W * cta / ctas;
+  hi = W * (cta + 1) / ctas;
+  return true;
+}
+
 // Header of a CTA that leaves the item of piece c unfinished: the CTAs from this one on that
-// hold its parts, and where its rows go.  {parts, tile head, first token, tokens}.
-__device__ __forceinline__ int4 paged_header(const PagedSched& s, const PagedPiece& c,
-                                             long long W, long long ctas, int cta) {
-  const long long last = (c.item_end * ctas + W - 1) / W - 1;  // the CTA that reaches its end
-  return make_int4(static_cast<int>(last - cta + 1), c.h, s.rec[c.rec].tok0, s.rec[c.rec].ntok);
+// hold its parts, and where its rows go.  {parts, tile head, first token, tokens}.  Called by the
+// thread that wrote the empty header.
+template <int C>
+__device__ __forceinline__ void paged_header(const PagedParams& p, const PagedSched& s,
+                                             const PagedRec& r, int h, int cta) {
+  const long long end = r.lin + static_cast<long long>(h) * (r.n + C) + r.n;  // of its tiles
+  const long long last = (end * s.ctas + s.W - 1) / s.W - 1;  // the CTA that reaches it
+  p.ws_head[cta] = make_int4(static_cast<int>(last - cta + 1), h, r.tok0, r.ntok);
 }
 
 // Natural-log log-sum-exp of a row from its maximum (log2 units) and sum; -inf without keys.
@@ -232,87 +294,151 @@ __device__ __forceinline__ float paged_lse(float m, float l) {
 
 // ---------------------------------------------------------------------------------- join
 // Block (c, j) joins rows of the item that CTA c left unfinished: O = sum_i 2^(m_i - m) O_i / l,
-// l = sum_i 2^(m_i - m) l_i, over the parts in key order.  WPR warps share a row: they take every
-// WPR-th part, eight of them loaded at once, and add their sums in warp order.  WPR = 4 where
-// items have few rows and many parts (decoding: 12.2 us for the call of one request of 2000 keys,
-// against 19.7 us with a part's loads waiting for the one before), 1 where they have many rows.
-// Bound by the launch and three dependent loads; launched to overlap the end of the kernel before.
+// l = sum_i 2^(m_i - m) l_i, over the parts in key order; part 0 is slot 1 of CTA c, part i slot 0
+// of CTA c + i.  Bound by the launch and two dependent loads (the header, the parts), as long as
+// the grid is about one wave and a warp has all its loads in flight; launched to overlap the end
+// of the kernel before.  Two forms:
+//   few rows, many parts (decoding): four warps share a row; each takes every fourth part, eight
+//     of them loaded at once, and they meet in warp order;
+//   many rows, two or three parts (chunks): each warp has four rows (eight where a row is 16
+//     lanes wide) in flight.  One row per warp and 32 blocks per item were 8 waves of blocks and
+//     40 us behind a 245 us kernel (8192 causal tokens, d = 128).
 constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_ROWS = 4;  // rows in flight per group of lanes
 
-template <typename T, int WPR>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_kernel(const PagedParams p) {
+__device__ __forceinline__ size_t paged_part(int cta, int i) {
+  return i == 0 ? static_cast<size_t>(cta) * 2 + 1 : static_cast<size_t>(cta + i) * 2;
+}
+
+// Running join of one row, four columns per lane.
+struct PagedJoin {
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void raise(float to) {  // to >= m
+    const float f = to == m ? 1.0f : exp2f(m - to);
+    m = to;
+    l *= f;
+    acc.x *= f;
+    acc.y *= f;
+    acc.z *= f;
+    acc.w *= f;
+  }
+  __device__ __forceinline__ void add(float2 ml, float4 a) {  // ml.x <= m
+    if (ml.x == -INFINITY) return;
+    const float w = exp2f(ml.x - m);
+    l = fmaf(w, ml.y, l);
+    acc.x = fmaf(w, a.x, acc.x);
+    acc.y = fmaf(w, a.y, acc.y);
+    acc.z = fmaf(w, a.z, acc.z);
+    acc.w = fmaf(w, a.w, acc.w);
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(const PagedParams& p, long long row, int col) const {
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    T* op = static_cast<T*>(p.o) + row * p.d;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (col + c < p.d) op[col + c] = from_f<T>(o[c]);
+    if (col == 0) p.lse[row] = paged_lse(m, l);
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_few_kernel(const PagedParams p) {
+  constexpr int WPR = 4, DEPTH = 8;
   __shared__ float4 s_acc[JOIN_WARPS][32];
-  __shared__ float s_l[JOIN_WARPS];
+  __shared__ float2 s_ml[JOIN_WARPS];
   grid_dep_wait();
   const int cta = blockIdx.x;
   const int4 head = p.ws_head[cta];
   if (head.x <= 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = head.w * p.G, parts = head.x;
-  const size_t first = static_cast<size_t>(cta) * 2 + 1;
-  constexpr int AT_ONCE = JOIN_WARPS / WPR;
-  for (int r0 = blockIdx.y * AT_ONCE; r0 < rows; r0 += gridDim.y * AT_ONCE) {
+  for (int r0 = blockIdx.y * (JOIN_WARPS / WPR); r0 < rows; r0 += gridDim.y * (JOIN_WARPS / WPR)) {
     const int r = r0 + warp / WPR;
     const int qh = paged_row_head(p, head.y, r, rows);
-    // part i: slot 1 of this CTA, then slot 0 of the ones after it
-    auto stats = [&](int i) { return (i == 0 ? first : first + 2 * i - 1) * p.rows_cap + r; };
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);  // columns 4 lane ..
-    if (qh >= 0) {
-      for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.ws_ml[stats(i)].x);
+    PagedJoin j;
+    for (int i0 = qh >= 0 ? warp % WPR : parts; i0 < parts; i0 += DEPTH * WPR) {
+      float4 part[DEPTH];
+      float2 ml[DEPTH];
+      float top = j.m;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      constexpr int DEPTH = 8;
-      for (int i0 = warp % WPR; i0 < parts; i0 += DEPTH * WPR) {
-        float4 part[DEPTH];
-        float2 ml[DEPTH];
-#pragma unroll
-        for (int k = 0; k < DEPTH; ++k) {
-          const int i = i0 + k * WPR;
-          if (i >= parts) continue;
-          ml[k] = p.ws_ml[stats(i)];
-          const float* src = p.ws_o + stats(i) * p.ws_pitch + 4 * lane;
-          part[k] = 4 * lane < p.d ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int k = 0; k < DEPTH; ++k) {
-          if (i0 + k * WPR >= parts || ml[k].x == -INFINITY) continue;
-          const float w = exp2f(ml[k].x - m);
-          l = fmaf(w, ml[k].y, l);
-          acc.x = fmaf(w, part[k].x, acc.x);
-          acc.y = fmaf(w, part[k].y, acc.y);
-          acc.z = fmaf(w, part[k].z, acc.z);
-          acc.w = fmaf(w, part[k].w, acc.w);
-        }
+      for (int k = 0; k < DEPTH; ++k) {
+        const int i = i0 + k * WPR;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        part[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i >= parts) continue;
+        const size_t at = paged_part(cta, i) * p.rows_cap + r;
+        ml[k] = p.ws_ml[at];
+        if (4 * lane < p.d) part[k] = *reinterpret_cast<const float4*>(p.ws_o + at * p.ws_pitch + 4 * lane);
       }
-    }
-    if constexpr (WPR > 1) {
-      s_acc[warp][lane] = acc;
-      if (lane == 0) s_l[warp] = l;
-      __syncthreads();
-      if (warp % WPR == 0) {
 #pragma unroll
-        for (int w = 1; w < WPR; ++w) {
-          const float4 a = s_acc[warp + w][lane];
-          acc.x += a.x;
-          acc.y += a.y;
-          acc.z += a.z;
-          acc.w += a.w;
-          l += s_l[warp + w];
-        }
+      for (int k = 0; k < DEPTH; ++k) top = fmaxf(top, ml[k].x);
+      j.raise(top);
+#pragma unroll
+      for (int k = 0; k < DEPTH; ++k) j.add(ml[k], part[k]);
+    }
+    s_acc[warp][lane] = j.acc;
+    if (lane == 0) s_ml[warp] = make_float2(j.m, j.l);
+    __syncthreads();
+    if (warp % WPR == 0 && qh >= 0) {
+      float top = j.m;
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) top = fmaxf(top, s_ml[warp + w].x);
+      j.raise(top);
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) j.add(s_ml[warp + w], s_acc[warp + w][lane]);
+      j.store<T>(p, static_cast<long long>(head.z + r / p.G) * p.H + qh, 4 * lane);
+    }
+    __syncthreads();  // s_acc is rewritten for the next rows
+  }
+}
+
+// LPR: lanes per row, 4 LPR >= d.
+template <typename T, int LPR>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_rows_kernel(const PagedParams p) {
+  constexpr int DEPTH = 2;
+  grid_dep_wait();
+  const int cta = blockIdx.x;
+  const int4 head = p.ws_head[cta];
+  if (head.x <= 0) return;
+  const int rows = head.w * p.G, parts = head.x;
+  const int group = threadIdx.x / LPR, col = 4 * (threadIdx.x % LPR);
+  constexpr int GROUPS = JOIN_WARPS * 32 / LPR;
+  const int r0 = blockIdx.y * (GROUPS * JOIN_ROWS) + group;  // rows r0, r0 + GROUPS, ..
+  PagedJoin j[JOIN_ROWS];
+  for (int i0 = 0; i0 < parts; i0 += DEPTH) {
+    float4 part[JOIN_ROWS][DEPTH];
+    float2 ml[JOIN_ROWS][DEPTH];
+#pragma unroll
+    for (int k = 0; k < JOIN_ROWS; ++k)
+#pragma unroll
+      for (int e = 0; e < DEPTH; ++e) {
+        const int r = r0 + k * GROUPS;
+        ml[k][e] = make_float2(-INFINITY, 0.f);
+        part[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r >= rows || i0 + e >= parts) continue;
+        const size_t at = paged_part(cta, i0 + e) * p.rows_cap + r;
+        ml[k][e] = p.ws_ml[at];
+        if (col < p.d) part[k][e] = *reinterpret_cast<const float4*>(p.ws_o + at * p.ws_pitch + col);
       }
-      __syncthreads();  // s_acc is rewritten for the next rows
-    }
-    if (qh >= 0 && warp % WPR == 0) {
-      const long long row = static_cast<long long>(head.z + r / p.G) * p.H + qh;
-      const float inv = l == 0.f ? 0.f : 1.0f / l;
-      T* op = static_cast<T*>(p.o) + row * p.d + 4 * lane;
-      const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (4 * lane + c < p.d) op[c] = from_f<T>(o[c]);
-      if (lane == 0) p.lse[row] = paged_lse(m, l);
+    for (int k = 0; k < JOIN_ROWS; ++k) {
+      float top = j[k].m;
+#pragma unroll
+      for (int e = 0; e < DEPTH; ++e) top = fmaxf(top, ml[k][e].x);
+      j[k].raise(top);
+#pragma unroll
+      for (int e = 0; e < DEPTH; ++e) j[k].add(ml[k][e], part[k][e]);
     }
+  }
+#pragma unroll
+  for (int k = 0; k < JOIN_ROWS; ++k) {
+    const int r = r0 + k * GROUPS;
+    const int qh = paged_row_head(p, head.y, r, rows);
+    if (qh >= 0 && col < p.d)
+      j[k].store<T>(p, static_cast<long long>(head.z + r / p.G) * p.H + qh, col);
   }
 }
 

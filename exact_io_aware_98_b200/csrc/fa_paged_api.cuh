@@ -96,12 +96,15 @@ size_t paged_ws_bytes(long long T, int group, int d) {
   return n;
 }
 
-// WPR: warps per row of a split item.
-template <typename T, int WPR>
-int launch_join(const fa::PagedParams& p, int ctas, cudaStream_t s) {
+// few: items have few rows (decoding).
+template <typename T>
+int launch_join(const fa::PagedParams& p, int ctas, bool few, cudaStream_t s) {
+  const int lpr = p.d <= 64 ? 16 : 32;
+  const int rows = few ? fa::JOIN_WARPS / 4 : fa::JOIN_WARPS * 32 / lpr * fa::JOIN_ROWS;  // of a block
+  auto* kern = few ? fa::fa_paged_join_few_kernel<T>
+                   : (lpr == 16 ? fa::fa_paged_join_rows_kernel<T, 16> : fa::fa_paged_join_rows_kernel<T, 32>);
   cudaLaunchConfig_t cfg = {};
-  const int at_once = fa::JOIN_WARPS / WPR;
-  cfg.gridDim = dim3(ctas, std::min((p.rows_cap + at_once - 1) / at_once, 16));
+  cfg.gridDim = dim3(ctas, (p.rows_cap + rows - 1) / rows);
   cfg.blockDim = dim3(fa::JOIN_WARPS * 32);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -109,7 +112,7 @@ int launch_join(const fa::PagedParams& p, int ctas, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::fa_paged_join_kernel<T, WPR>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "fa_paged_join_kernel: %s", cudaGetErrorString(e));
   return check_launch("fa_paged_join_kernel");
 }
@@ -138,7 +141,7 @@ int launch_paged_simt(fa::PagedParams p, int H_kv, void* ws, cudaStream_t s) {
   if (rc != FA_OK) return rc;
   fa::fa_paged_simt_kernel<T, WR, WK><<<v.ctas, 128, smem, s>>>(p);
   if ((rc = check_launch("fa_paged_simt_kernel")) != FA_OK) return rc;
-  return launch_join<T, (WK > 1 ? 4 : 1)>(p, v.ctas, s);
+  return launch_join<T>(p, v.ctas, WK > 1, s);
 }
 
 // 4-D view [page][H_kv][page_size][d] bf16 of a cache, 128-byte swizzled boxes of 64 columns and
@@ -179,7 +182,7 @@ int launch_paged_decode(fa::PagedParams p, int H_kv, int page_size, void* ws, cu
     fa::fa_paged_decode_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mk, mv, p);
     if ((rc = check_launch("fa_paged_decode_sm100_kernel")) != FA_OK) return rc;
   }
-  return launch_join<__nv_bfloat16, 4>(p, v.ctas, s);
+  return launch_join<__nv_bfloat16>(p, v.ctas, true, s);
 }
 
 // 3-D view [T][H][d] bf16 of the packed queries, 128-byte swizzled boxes of 64 columns, `heads`
@@ -220,7 +223,7 @@ int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cud
     fa::fa_paged_chunk_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mq, mqf, mk, mv, few, p);
     if ((rc = check_launch("fa_paged_chunk_sm100_kernel")) != FA_OK) return rc;
   }
-  return launch_join<__nv_bfloat16, 1>(p, v.ctas, s);
+  return launch_join<__nv_bfloat16>(p, v.ctas, false, s);
 }
 
 }  // namespace
@@ -490,6 +493,7 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
   p.group = H / H_kv;
   p.d = d;
   p.vec = d % 4 == 0 && (num_pages == 1 || ((k_page_stride * es) % 16 == 0 && (v_page_stride * es) % 16 == 0));
+  p.o_al32 = aligned_to(o, 32) ? 1 : 0;
   p.page_shift = shift;
   p.num_pages = num_pages;
   p.max_pages = max_pages;

@@ -27,11 +27,20 @@ enum : int {
   SITE_PCH_SM_O = 58, SITE_PCH_SM_V = 59
 };
 
+// One 32-byte sector per lane (the address 32-byte aligned): a warp whose lanes write a row each
+// takes half as many store instructions as with 16-byte stores.
+__device__ __forceinline__ void st_global_256(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                              uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a), "r"(b), "r"(c),
+               "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
+
 template <int D>
 struct PagedChunkLayout {
   static constexpr int R = 256;
   static constexpr int BN = D == 64 ? 64 : 128;     // keys per tile
-  static constexpr int KT = BN;
+  static constexpr int C = 3;                       // an item's constant, in key tiles
   static constexpr int CTAS_PER_SM = BN == 64 ? 2 : 1;
   static constexpr int THREADS = 320;
   static constexpr int KST = BN == 64 ? 4 : 3;      // K ring depth
@@ -40,14 +49,14 @@ struct PagedChunkLayout {
   static constexpr int Q_SUB = 256 * 128;           // bytes of 256 Q rows x 64 columns
   static constexpr int KV_SUB = BN * 128;
   static constexpr int KV_TILE = BN * D * 2;
-  static constexpr int INFO = 8;                    // ring of per-tile page marks
+  static constexpr int INFO = 8;                    // ring of per-tile page marks (see s_info)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = OFF_Q + SUB * Q_SUB;
   static constexpr int OFF_V = OFF_K + KST * KV_TILE;
   static constexpr int OFF_BAR = OFF_V + VST * KV_TILE;
   // q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], s_full[2], p_full[2],
-  // o_done[2], p2_full[2], info[INFO], fin
-  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 8 + INFO + 1;
+  // o_done[2], p2_full[2], fin
+  static constexpr int NBAR = 2 + 2 * KST + 2 * VST + 8 + 1;
   static constexpr int OFF_INFO = OFF_BAR + NBAR * 8;
   static constexpr int OFF_MISC = OFF_INFO + INFO * 4;
   static constexpr int OFF_SCHED = (OFF_MISC + 8 + 15) / 16 * 16;
@@ -58,38 +67,45 @@ struct PagedChunkLayout {
   static constexpr uint32_t TMEM_COLS = 2 * BN + 2 * D <= 256 ? 256 : 512;
   static constexpr uint32_t O_COL0 = 2 * BN;
   static_assert(O_COL0 + 2 * D <= TMEM_COLS, "TMEM budget");
-  // the load warp can be this many tiles ahead of a softmax warpgroup at most
+  // the load warp can be this many tiles ahead of a softmax warpgroup at most: P of tile t must
+  // have been handed over before the scores of tile t + 2 can be issued
   static_assert(KST + 2 < INFO, "page marks are read before they are rewritten");
-  static constexpr int EMU_EVERY = 4;               // one P pair in this many on the FMA pipe
   __device__ static constexpr uint32_t s_col(int w) { return static_cast<uint32_t>(w) * BN; }
 };
 
-// What the roles need to know of a piece.
+// What the roles need to know of a piece: key tiles [a, b) are in it, of which those below n0 (n1)
+// hold a key that a row of Q tile 0 (1) may see.  Tiles from max(n0, n1) on (only the one tile of
+// an item without keys) are passed over by all roles.
 struct PagedChunkPiece {
-  PagedPiece pc;
-  PagedRec rc;
-  int rows;      // rows of the tile that exist
-  int keys;      // keys that its rows can see between them
-  int keys_w0;   // ... the rows of Q tile 0
+  int rec, h, a, b;
+  int n0, n1;
 };
 
-__device__ __forceinline__ PagedChunkPiece paged_chunk_piece(const PagedParams& p,
-                                                             const PagedSched& s, long long x,
-                                                             int rec) {
-  PagedChunkPiece c;
-  c.pc = paged_piece(p, s, x, rec);
-  c.rc = s.rec[c.pc.rec];
-  c.rows = c.rc.ntok * p.G;
-  c.keys = paged_keys(p.causal, c.rc.kv, c.rc.pos0, c.rc.ntok);
-  c.keys_w0 = c.rows <= 128 ? c.keys
-                            : paged_keys(p.causal, c.rc.kv, c.rc.pos0, 127 / p.G + 1);
+template <int BN>
+__device__ __forceinline__ PagedChunkPiece paged_chunk_piece(const PagedParams& p, const PagedSched& s,
+                                                             const PagedPiece& pc) {
+  const PagedRec& rc = s.rec[pc.rec];
+  PagedChunkPiece c = {pc.rec, pc.h, pc.a, pc.b, 0, 0};
+  const int keys = paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok);
+  if (rc.ntok * p.G > 128) {
+    c.n0 = (paged_keys(p.causal, rc.kv, rc.pos0, 127 / p.G + 1) + BN - 1) / BN;
+    c.n1 = (keys + BN - 1) / BN;
+  } else {
+    c.n0 = (keys + BN - 1) / BN;
+  }
   return c;
 }
 
-// bit w set: key tile j holds a key that a row of Q tile w may see
+// Scores of the marked 16-key groups become -inf, in TMEM and before they are read, so that the
+// rare case costs the loop one test (masking them in registers cost it 4 %).  The whole warp.
 template <int BN>
-__device__ __forceinline__ int paged_chunk_flags(const PagedChunkPiece& c, int j) {
-  return (j * BN < c.keys_w0 ? 1 : 0) | (c.rows > 128 && j * BN < c.keys ? 2 : 0);
+__device__ __forceinline__ void paged_hide(uint32_t t_s, int marks) {
+  uint32_t hidden[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) hidden[i] = __float_as_uint(-INFINITY);
+  for (int g = 0; g < BN / 16; ++g)
+    if ((marks >> g) & 1) tmem_st16(t_s + 16 * g, hidden);
+  tmem_st_wait();
 }
 
 template <int D>
@@ -100,7 +116,7 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
                             const __grid_constant__ CUtensorMap tm_v, const int few_tokens,
                             const PagedParams p) {
   using L = PagedChunkLayout<D>;
-  constexpr int BN = L::BN;
+  constexpr int BN = L::BN, C = L::C;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -114,8 +130,9 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
   uint64_t* bar_pf = bar_sf + 2;
   uint64_t* bar_od = bar_pf + 2;
   uint64_t* bar_p2 = bar_od + 2;
-  uint64_t* bar_info = bar_p2 + 2;
-  uint64_t* bar_fin = bar_info + L::INFO;
+  uint64_t* bar_fin = bar_p2 + 2;
+  // bits of 16-key groups of a tile whose page the table does not name; written before the tile's
+  // K is awaited, read once its scores are there
   volatile int* s_info = reinterpret_cast<volatile int*>(smem + L::OFF_INFO);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
@@ -124,13 +141,9 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int tpt = L::R / p.G;  // tokens per tile; G <= 256
 
   grid_dep_launch();
-  const long long W = paged_total<BN, 320>(p, tpt, sched);
-  const long long ctas = min(static_cast<long long>(gridDim.x), W);
   const int cta = blockIdx.x;
-  if (cta >= ctas) {
-    if (threadIdx.x == 0) p.ws_head[cta] = make_int4(0, 0, 0, 0);
-    return;
-  }
+  long long x, hi;
+  if (!paged_share<BN, C, 320>(p, tpt, sched, x, hi)) return;
   if (threadIdx.x == 0) {
     mbar_init(bar_qf, 1);
     mbar_init(bar_qe, 1);
@@ -148,7 +161,6 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
       mbar_init(&bar_p2[w], 128);
       mbar_init(&bar_od[w], 1);
     }
-    for (int s = 0; s < L::INFO; ++s) mbar_init(&bar_info[s], 1);
     mbar_init(bar_fin, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -162,9 +174,6 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  long long x = paged_cut(W, cta, ctas);
-  const long long hi = paged_cut(W, cta + 1, ctas);
-  int4 header = make_int4(0, 0, 0, 0);
   bool ok = true;
   // running counts of each role: key tiles and pieces with keys (every role), S / PV per Q tile
   int it = 0, qn = 0, cnt0 = 0, cnt1 = 0;
@@ -172,8 +181,11 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
   int prev_flags = 0, prev_vs = 0, prev_it = 0, prev_acc = 0;
 
   while (x < hi) {
-    paged_list<BN, 320>(p, tpt, x, hi, sched);
+    paged_list<BN, C, 320>(p, tpt, x, hi, sched);
     const long long stop = sched.stop;
+    PagedPieces<C> pieces;
+    pieces.start(p, sched, x);
+    PagedPiece pc;
     if (warp == 8) {
       // ------------------------------------------------------------------ TMA producer
       // every lane keeps its page of a tile; the boxes of a tile are issued by one lane each
@@ -181,25 +193,24 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
       const int np = BN / box;
       const int part = lane / (np * L::SUB);       // 0: K or V by turns, more: idle
       const int pg = lane / L::SUB % np, sub = lane % L::SUB;
-      int rec = 0;
-      while (x < stop && ok) {
-        const PagedChunkPiece c = paged_chunk_piece(p, sched, x, rec);
-        rec = c.pc.rec;
-        x += c.pc.b - c.pc.a;
+      while (ok && pieces.next(p, sched, pc)) {
+        const PagedChunkPiece c = paged_chunk_piece<BN>(p, sched, pc);
+        const PagedRec rc = sched.rec[c.rec];
         bool first = true;
-        const int32_t* table = p.table + c.rc.b * p.table_stride;
-        const int h = c.pc.h / p.splits, q0 = h * p.group + (c.pc.h - h * p.splits) * p.G;
+        const int32_t* table = p.table + rc.b * p.table_stride;
+        const int keys = paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok);
+        const int h = c.h / p.splits, q0 = h * p.group + (c.h - h * p.splits) * p.G;
         auto page_id = [&](int j) -> int {
           const int k = j * BN + pg * box;
-          return k < c.keys ? table[k >> p.page_shift] : -1;
+          return k < keys ? table[k >> p.page_shift] : -1;
         };
-        int id = page_id(c.pc.a);
-        for (int j = c.pc.a; j < c.pc.b; ++j) {
+        int id = page_id(c.a);
+        const int j_end = min(c.b, max(c.n0, c.n1));
+        for (int j = c.a; j < j_end; ++j) {
           const int id_now = id;
-          if (j + 1 < c.pc.b) id = page_id(j + 1);
-          if (paged_chunk_flags<BN>(c, j) == 0) continue;
+          if (j + 1 < j_end) id = page_id(j + 1);
           const bool there = id_now >= 0 && id_now < p.num_pages;
-          const bool behind = j * BN + pg * box >= c.keys;
+          const bool behind = j * BN + pg * box >= keys;
           // groups of 16 keys whose page the table does not name
           const bool bad16 = __shfl_sync(0xffffffffu, !there && !behind, (16 * (lane & 7) / box % np) * L::SUB);
           const unsigned bad = __ballot_sync(0xffffffffu, lane < BN / 16 && bad16);
@@ -211,7 +222,6 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           if (!ok) break;
           if (lane == 0) {
             s_info[it % L::INFO] = static_cast<int>(bad);
-            mbar_arrive(&bar_info[it % L::INFO]);
             mbar_arrive_expect_tx(&bar_kf[ks], L::KV_TILE);
           }
           __syncwarp();
@@ -225,11 +235,11 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
               ok = __all_sync(0xffffffffu, mbar_wait(bar_qe, (qn - 1) & 1, abort_flag, SITE_PCH_LOAD_EMPTY));
             if (ok) {
               if (lane == 0) {
-                const bool few = c.rc.ntok <= few_tokens;
+                const bool few = rc.ntok <= few_tokens;
                 mbar_arrive_expect_tx(bar_qf, L::SUB * (few ? few_tokens : tpt) * p.G * 128);
                 for (int s = 0; s < L::SUB; ++s)
                   tma_load_3d(smem + L::OFF_Q + s * L::Q_SUB, few ? &tm_q_few : &tm_q, bar_qf, s * 64,
-                              q0, c.rc.tok0);
+                              q0, rc.tok0);
               }
               ++qn;
             }
@@ -249,7 +259,6 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           cnt0 = it;  // V tiles issued
         }
       }
-      x = stop;
     } else if (warp == 9) {
       // ------------------------------------------------------------------ MMA issuer
       constexpr uint32_t idesc_s = idesc_bf16_f32(128, BN, false, false);
@@ -315,16 +324,13 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         prev_flags = 0;
       };
-      int rec = 0;
-      while (x < stop && ok) {
-        const PagedChunkPiece c = paged_chunk_piece(p, sched, x, rec);
-        rec = c.pc.rec;
-        x += c.pc.b - c.pc.a;
+      while (ok && pieces.next(p, sched, pc)) {
+        const PagedChunkPiece c = paged_chunk_piece<BN>(p, sched, pc);
         bool first = true;
         int acc = 0;  // bit w: O_w of this piece has been started
-        for (int j = c.pc.a; ok && j < c.pc.b; ++j) {
-          const int f = paged_chunk_flags<BN>(c, j);
-          if (f == 0) continue;
+        const int j_end = min(c.b, max(c.n0, c.n1));
+        for (int j = c.a; ok && j < j_end; ++j) {
+          const int f = (j < c.n0 ? 1 : 0) | (j < c.n1 ? 2 : 0);  // the Q tiles that see this tile
           const int ks = it % L::KST;
           if (first) {
             // the piece before ends here: its last P V must not wait for this piece's loads
@@ -355,9 +361,8 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         if (ok && !first) mma_commit_w(bar_qe);  // every S of this piece has read Q
       }
-      x = stop;
       flush_pv();  // the softmax warpgroups finish the listed pieces before the next list
-      if (x >= hi) {
+      if (stop >= hi) {
         // all MMAs issued by this warp have completed before TMEM is released
         mma_commit_w(bar_fin);
         mbar_wait_w(bar_fin, 0, abort_flag, SITE_PCH_MMA_FIN);
@@ -371,41 +376,38 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
       const uint32_t t_o = tmem + t_lane + L::O_COL0 + w * D;
       const float scale2 = p.scale2;
       const int my_tok = r / p.G, warp_tok = (128 * w + 32 * qw) / p.G;
-      int rec = 0;
-      while (x < stop) {
-        const PagedChunkPiece c = paged_chunk_piece(p, sched, x, rec);
-        rec = c.pc.rec;
+      while (pieces.next(p, sched, pc)) {
+        const PagedChunkPiece c = paged_chunk_piece<BN>(p, sched, pc);
         float m_ref = -INFINITY, l = 0.f;
-        bool any = false;
-        // keys of this row, and of the warp's first row (the fewest)
-        const int n_row = p.causal ? min(c.keys, c.rc.pos0 + my_tok + 1) : c.keys;
-        const int n_min = p.causal ? min(c.keys, c.rc.pos0 + warp_tok + 1) : c.keys;
-        for (int j = c.pc.a; j < c.pc.b && ok; ++j) {
-          const int f = paged_chunk_flags<BN>(c, j);
-          if (f == 0) continue;
-          const int my_it = it++;
-          if (!((f >> w) & 1)) continue;
-          bool got = mbar_wait(&bar_sf[w], cnt0 & 1, abort_flag, SITE_PCH_SM_S);
-          got = got && mbar_wait(&bar_info[my_it % L::INFO], (my_it / L::INFO) & 1, abort_flag, SITE_PCH_SM_S);
+        const int cnt_piece = cnt0;
+        const int kv = sched.rec[c.rec].kv;
+        int n_row, n_min;  // keys of this row, and of the warp's first row (the fewest)
+        {
+          const PagedRec& rc = sched.rec[c.rec];
+          n_row = p.causal ? min(kv, rc.pos0 + my_tok + 1) : kv;
+          n_min = p.causal ? min(kv, rc.pos0 + warp_tok + 1) : kv;
+        }
+        const int j_end = min(c.b, w == 0 ? c.n0 : c.n1);
+        for (int j = c.a; j < j_end && ok; ++j) {
+          const int my_it = it + (j - c.a);
+          const bool got = mbar_wait(&bar_sf[w], cnt0 & 1, abort_flag, SITE_PCH_SM_S);
           if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
           tc_fence_after();
           constexpr int NC = BN / 32;
+          if (const int bad = s_info[my_it % L::INFO]) paged_hide<BN>(t_s, bad);
           uint32_t rg[NC][32];
 #pragma unroll
           for (int cc = 0; cc < NC; ++cc) tmem_ld32(t_s + 32 * cc, rg[cc]);
           const int k0 = j * BN;
-          const int bad = s_info[my_it % L::INFO];
-          const bool edge = bad != 0 || k0 + BN > n_min;
           tmem_ld_wait();
 #pragma unroll
           for (int cc = 0; cc < NC; ++cc) reg_fence(rg[cc]);
-          if (edge) {
+          if (k0 + BN > n_min) {
 #pragma unroll
             for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (k0 + 32 * cc + i >= n_row || ((bad >> (2 * cc + i / 16)) & 1))
-                  rg[cc][i] = __float_as_uint(-INFINITY);
+                if (k0 + 32 * cc + i >= n_row) rg[cc][i] = __float_as_uint(-INFINITY);
           }
           float mc[8];
 #pragma unroll
@@ -421,10 +423,10 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           if (tmax > m_ref + 8.0f) m_new = tmax;  // also taken when m_ref is still -inf
           const float alpha = (m_new == m_ref) ? 1.0f : ex2_approx(m_ref - m_new);
           const float neg_base = (m_new == -INFINITY) ? 0.0f : -m_new;
-          const bool rescale = any && (m_new != m_ref);
+          const bool rescale = cnt0 != cnt_piece && (m_new != m_ref);
           m_ref = m_new;
           float ra[4] = {0.f, 0.f, 0.f, 0.f}, rb[4] = {0.f, 0.f, 0.f, 0.f};
-          auto exp_chunk = [&](bool use_fma, int cc) {
+          auto exp_chunk = [&](int cc) {
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -432,12 +434,8 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
               float x0, x1, p0, p1;
               ffma2(x0, x1, __uint_as_float(rg[cc][2 * i]), __uint_as_float(rg[cc][2 * i + 1]), scale2,
                     scale2, neg_base, neg_base);
-              if (use_fma && (q % L::EMU_EVERY) == L::EMU_EVERY - 1) {
-                exp2_fma2(p0, p1, x0, x1);
-              } else {
-                p0 = ex2_approx(x0);
-                p1 = ex2_approx(x1);
-              }
+              p0 = ex2_approx(x0);
+              p1 = ex2_approx(x1);
               fadd2(ra[q & 3], rb[q & 3], ra[q & 3], rb[q & 3], p0, p1);
               pk[i] = pack_bf16x2(p0, p1);
             }
@@ -464,12 +462,12 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           };
           // V rows behind the request's last key in its last page: cleared (both warpgroups write
           // the same zeros, each before its own P goes out)
-          const int stale = c.rc.kv - k0;
-          if (stale < BN && (c.rc.kv & ((1 << p.page_shift) - 1)) != 0) {
+          const int stale = kv - k0;
+          if (stale < BN && (kv & ((1 << p.page_shift) - 1)) != 0) {
             const int vs = my_it % L::VST;
             const bool gv = mbar_wait(&bar_vf[vs], (my_it / L::VST) & 1, abort_flag, SITE_PCH_SM_V);
             if (!__all_sync(0xffffffffu, gv)) { ok = false; break; }
-            const int page_end = ((c.rc.kv >> p.page_shift) + 1) << p.page_shift;
+            const int page_end = ((kv >> p.page_shift) + 1) << p.page_shift;
             const int n = (min(BN, page_end - k0) - stale) * 8 * L::SUB;
             for (int e = 32 * qw + lane; e < n; e += 128) {
               const int row = stale + e / (8 * L::SUB), q = e % (8 * L::SUB);
@@ -479,40 +477,33 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
             fence_proxy_async_smem();
           }
           constexpr int C1 = L::SPLIT_P ? NC / 2 : NC;
-          if (edge) {
 #pragma unroll
-            for (int cc = 0; cc < C1; ++cc) exp_chunk(false, cc);
-          } else {
-#pragma unroll
-            for (int cc = 0; cc < C1; ++cc) exp_chunk(true, cc);
-          }
+          for (int cc = 0; cc < C1; ++cc) exp_chunk(cc);
           rescale_o();
           hand_over(&bar_pf[w]);
           if constexpr (L::SPLIT_P) {
-            if (edge) {
 #pragma unroll
-              for (int cc = C1; cc < NC; ++cc) exp_chunk(false, cc);
-            } else {
-#pragma unroll
-              for (int cc = C1; cc < NC; ++cc) exp_chunk(true, cc);
-            }
+            for (int cc = C1; cc < NC; ++cc) exp_chunk(cc);
             hand_over(&bar_p2[w]);
           }
           l = alpha * l + ((ra[0] + ra[1]) + (ra[2] + ra[3]) + ((rb[0] + rb[1]) + (rb[2] + rb[3])));
-          any = true;
           ++cnt0;
         }
         // ---------------------------------------------------------------- write the piece out
-        if (ok && 128 * w < c.rows) {
+        it += max(0, min(c.b, max(c.n0, c.n1)) - c.a);
+        const PagedRec rc = sched.rec[c.rec];
+        const int rows = rc.ntok * p.G;
+        const bool any = cnt0 != cnt_piece;
+        const bool whole = c.a == 0 && c.b == rc.n;
+        if (ok && 128 * w < rows) {
           if (any) {
             const bool got = mbar_wait(&bar_od[w], (cnt0 - 1) & 1, abort_flag, SITE_PCH_SM_O);
             ok = __all_sync(0xffffffffu, got);
             tc_fence_after();
           }
-          const bool whole = c.pc.a == 0 && c.pc.b == c.rc.n;
-          const size_t slot = paged_slot(cta, c.pc);
-          const int qh = ok ? paged_row_head(p, c.pc.h, r, c.rows) : -1;
-          const long long row = static_cast<long long>(c.rc.tok0 + my_tok) * p.H + qh;
+          const size_t slot = static_cast<size_t>(cta) * 2 + (c.a > 0 ? 0 : 1);
+          const int qh = ok ? paged_row_head(p, c.h, r, rows) : -1;
+          const long long row = static_cast<long long>(rc.tok0 + my_tok) * p.H + qh;
           const float inv = l == 0.f ? 0.0f : 1.0f / l;
 #pragma unroll
           for (int cc = 0; cc < D / 32; ++cc) {
@@ -527,20 +518,27 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
             }
             if (qh >= 0) {
               if (whole) {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * D + 32 * cc);
+                __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.o) + row * D + 32 * cc;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  uint32_t hh[4];
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t hh[8];
 #pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    hh[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]) * inv,
-                                        __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-                  dst[i] = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                  for (int e = 0; e < 8; ++e)
+                    hh[e] = pack_bf16x2(__uint_as_float(o[16 * i + 2 * e]) * inv,
+                                        __uint_as_float(o[16 * i + 2 * e + 1]) * inv);
+                  if (p.o_al32) {
+                    st_global_256(dst + 16 * i, hh[0], hh[1], hh[2], hh[3], hh[4], hh[5], hh[6], hh[7]);
+                  } else {
+                    *reinterpret_cast<uint4*>(dst + 16 * i) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                    *reinterpret_cast<uint4*>(dst + 16 * i + 8) = make_uint4(hh[4], hh[5], hh[6], hh[7]);
+                  }
                 }
               } else {
-                uint4* dst = reinterpret_cast<uint4*>(p.ws_o + (slot * p.rows_cap + r) * p.ws_pitch + 32 * cc);
+                float* dst = p.ws_o + (slot * p.rows_cap + r) * p.ws_pitch + 32 * cc;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                for (int i = 0; i < 4; ++i)
+                  st_global_256(dst + 8 * i, o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3], o[8 * i + 4],
+                                o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]);
               }
             }
           }
@@ -550,13 +548,12 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
           tc_fence_before();  // O has been read before this warpgroup's next P goes out
         }
-        if (c.pc.a == 0 && c.pc.b < c.rc.n) header = paged_header(sched, c.pc, W, ctas, cta);
-        x += c.pc.b - c.pc.a;
+        if (threadIdx.x == 0 && c.a == 0 && c.b < rc.n) paged_header<C>(p, sched, rc, c.h, cta);
       }
     }
+    x = stop;
     __syncthreads();  // the list is rewritten
   }
-  if (threadIdx.x == 0) p.ws_head[cta] = header;
   if (warp == 8) {
     // Never leave the CTA with a copy in flight (immediate in the normal path)
     if (qn > 0) mbar_wait_drain(bar_qf, (qn - 1) & 1, SITE_PCH_LOAD_DRAIN);

@@ -29,6 +29,7 @@ enum : int { SITE_PDEC_EMPTY = 40, SITE_PDEC_FULL = 41, SITE_PDEC_DRAIN = 42 };
 template <int D>
 struct PagedDecodeLayout {
   static constexpr int R = 16, KT = 64;
+  static constexpr int C = 1;                        // an item's constant, in key tiles
   static constexpr int WARPS = 8;                    // consumers
   static constexpr int THREADS = (WARPS + 1) * 32;
   static constexpr int SUB = D / 64;                 // 64-column (128-byte) sub-tiles
@@ -83,22 +84,21 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Walks the key tiles of the listed pieces in order.
+// Walks over the key tiles of the listed pieces in order.
+template <int C>
 struct PagedTileWalk {
-  long long x, stop;
+  PagedPieces<C> pieces;
   PagedPiece pc;
   int t;
-  __device__ __forceinline__ void start(const PagedParams& p, const PagedSched& s, long long x0) {
-    x = x0;
-    stop = s.stop;
-    pc = paged_piece(p, s, x, 0);
+  __device__ __forceinline__ bool start(const PagedParams& p, const PagedSched& s, long long x0) {
+    pieces.start(p, s, x0);
+    const bool any = pieces.next(p, s, pc);
     t = pc.a;
+    return any;
   }
   __device__ __forceinline__ bool next(const PagedParams& p, const PagedSched& s) {
     if (++t < pc.b) return true;
-    x += pc.b - pc.a;
-    if (x >= stop) return false;
-    pc = paged_piece(p, s, x, pc.rec);
+    if (!pieces.next(p, s, pc)) return false;
     t = pc.a;
     return true;
   }
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(PagedDecodeLayout<D>::THREADS, 1)
 fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
                              const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
   using L = PagedDecodeLayout<D>;
-  constexpr int KT = L::KT, ST = L::ST;
+  constexpr int KT = L::KT, ST = L::ST, C = L::C;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -130,21 +130,14 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
     *abort_flag = 0;
     fence_mbar_init();
   }
-  const long long W = paged_total<KT, L::THREADS>(p, tpt, sched);  // ends with a barrier
-  const long long ctas = min(static_cast<long long>(gridDim.x), W);
   const int cta = blockIdx.x;
-  if (cta >= ctas) {
-    if (tid == 0) p.ws_head[cta] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  long long x = paged_cut(W, cta, ctas);
-  const long long hi = paged_cut(W, cta + 1, ctas);
-  int4 header = make_int4(0, 0, 0, 0);
+  long long x, hi;
+  if (!paged_share<KT, C, L::THREADS>(p, tpt, sched, x, hi)) return;  // else: a barrier has passed
   int it = 0;      // tiles issued (producer) or passed (consumers) so far
   bool ok = true;
 
   while (x < hi) {
-    paged_list<KT, L::THREADS>(p, tpt, x, hi, sched);
+    paged_list<KT, C, L::THREADS>(p, tpt, x, hi, sched);
     const long long stop = sched.stop;
     if (warp == L::WARPS) {
       // ---------------------------------------------------------------- producer
@@ -153,17 +146,16 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int part = lane / (np * L::SUB);       // 0: K, 1: V, more: idle
       const int pg = lane / L::SUB % np, sub = lane % L::SUB;
       // this lane's page of a tile, and whether it lies behind the last key (not looked up then)
-      auto page_id = [&](const PagedTileWalk& w, bool& behind) -> int {
+      auto page_id = [&](const PagedTileWalk<C>& w, bool& behind) -> int {
         const PagedRec& rc = sched.rec[w.pc.rec];
         const int j = w.t * KT + pg * box;
         behind = j >= paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok);
         return behind ? -1 : p.table[rc.b * p.table_stride + (j >> p.page_shift)];
       };
-      PagedTileWalk w;
-      w.start(p, sched, x);
-      bool behind, behind_next = false;
-      int id = page_id(w, behind);
-      bool more = true;
+      PagedTileWalk<C> w;
+      bool more = w.start(p, sched, x);
+      bool behind = false, behind_next = false;
+      int id = more ? page_id(w, behind) : 0;
       while (more && ok) {
         const int h = w.pc.h / p.splits, row = (w.t * KT) & ((1 << p.page_shift) - 1);
         more = w.next(p, sched);
@@ -190,7 +182,6 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
         id = id_next;
         behind = behind_next;
       }
-      x = stop;
     } else {
       // ---------------------------------------------------------------- consumers
       const int group = warp >> 2, w4 = warp & 3;
@@ -198,10 +189,10 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
       float2* s_ml = reinterpret_cast<float2*>(smem + L::OFF_ML);
       float* s_o = reinterpret_cast<float*>(smem + L::OFF_O);
       const uint32_t q_addr = smem_u32(smem + L::OFF_Q);
-      int rec_at = 0;
-      while (x < stop) {
-        const PagedPiece pc = paged_piece(p, sched, x, rec_at);
-        rec_at = pc.rec;
+      PagedPieces<C> pieces;
+      pieces.start(p, sched, x);
+      PagedPiece pc;
+      while (pieces.next(p, sched, pc)) {
         const PagedRec rc = sched.rec[pc.rec];
         const int rows = rc.ntok * p.G;
         const int keys = paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok);
@@ -409,13 +400,12 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
           }
           named_bar_sync(1, L::WARPS * 32);  // s_o (and, after the last, s_ml and Q) may be rewritten
         }
-        if (pc.a == 0 && pc.b < rc.n) header = paged_header(sched, pc, W, ctas, cta);
-        x += pc.b - pc.a;
+        if (tid == 0 && pc.a == 0 && pc.b < rc.n) paged_header<C>(p, sched, rc, pc.h, cta);
       }
     }
+    x = stop;
     __syncthreads();  // the list is rewritten
   }
-  if (tid == 0) p.ws_head[cta] = header;
   if (warp == L::WARPS) {
     // no copy may be in flight when the CTA ends (immediate unless a wait gave up)
     for (int r = max(0, it - ST); r < it; ++r) mbar_wait_drain(&bar_full[r % ST], (r / ST) & 1, SITE_PDEC_DRAIN);

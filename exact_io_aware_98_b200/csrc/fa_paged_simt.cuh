@@ -16,6 +16,7 @@ namespace fa {
 template <int WR, int WK>
 struct PagedSimtLayout {
   static constexpr int R = 8 * WR, KT = 32 * WK;
+  static constexpr int C = 1;  // an item's constant, in key tiles
   // row pitch in floats of a d-column tile: an odd number of 16-byte chunks
   __host__ __device__ static int pitch(int d) { return (((d + 3) / 4) | 1) * 4; }
   // Q [R], K [KT], V [KT] rows, P [4 warps][32 keys][8 rows], row offsets 2 x [KT]; the K and V
@@ -38,7 +39,7 @@ __device__ __forceinline__ void cp_async_wait() {
 template <typename T, int WR, int WK>
 __global__ void __launch_bounds__(128) fa_paged_simt_kernel(const PagedParams p) {
   using L = PagedSimtLayout<WR, WK>;
-  constexpr int R = L::R, KT = L::KT, RW = 8;
+  constexpr int R = L::R, KT = L::KT, RW = 8, C = L::C;
   static_assert(WR * WK == 4, "four warps");
   extern __shared__ __align__(16) uint8_t smem_simt[];
   const int d = p.d, pitch = L::pitch(d), dv = (d + 3) / 4;
@@ -55,25 +56,17 @@ __global__ void __launch_bounds__(128) fa_paged_simt_kernel(const PagedParams p)
   grid_dep_launch();
   // zero the columns that pad d up to a multiple of 4 (read by the 16-byte accesses)
   for (int e = tid; e < (R + 2 * KT) * pitch; e += 128) s_q[e] = 0.f;
-  const long long W = paged_total<KT, 128>(p, tpt, sched);
-  const long long ctas = min(static_cast<long long>(gridDim.x), W);
   const int cta = blockIdx.x;
-  if (cta >= ctas) {
-    if (tid == 0) p.ws_head[cta] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  long long x = paged_cut(W, cta, ctas);
-  const long long hi = paged_cut(W, cta + 1, ctas);
-  int4 header = make_int4(0, 0, 0, 0);
+  long long x, hi;
+  if (!paged_share<KT, C, 128>(p, tpt, sched, x, hi)) return;
   float* my_p = s_p + warp * 32 * 8;
 
   while (x < hi) {
-    paged_list<KT, 128>(p, tpt, x, hi, sched);
-    const long long stop = sched.stop;
-    int rec_at = 0;
-    while (x < stop) {
-      const PagedPiece pc = paged_piece(p, sched, x, rec_at);
-      rec_at = pc.rec;
+    paged_list<KT, C, 128>(p, tpt, x, hi, sched);
+    PagedPieces<C> pieces;
+    pieces.start(p, sched, x);
+    PagedPiece pc;
+    while (pieces.next(p, sched, pc)) {
       const PagedRec rc = sched.rec[pc.rec];
       const int rows = rc.ntok * p.G;
       const int keys = paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok);
@@ -285,12 +278,11 @@ __global__ void __launch_bounds__(128) fa_paged_simt_kernel(const PagedParams p)
           if (lane == 0) p.ws_ml[slot * p.rows_cap + r] = make_float2(mm, ll);
         }
       }
-      if (pc.a == 0 && pc.b < rc.n) header = paged_header(sched, pc, W, ctas, cta);
-      x += pc.b - pc.a;
+      if (tid == 0 && pc.a == 0 && pc.b < rc.n) paged_header<C>(p, sched, rc, pc.h, cta);
     }
+    x = sched.stop;
     __syncthreads();  // the list is rewritten
   }
-  if (tid == 0) p.ws_head[cta] = header;
 }
 
 }  // namespace fa
