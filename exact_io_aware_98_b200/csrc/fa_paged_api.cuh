@@ -6,7 +6,6 @@
 namespace {
 
 constexpr int kSms = 148;            // B200; grids and workspaces are sized by it
-constexpr int kMaxPagedCtas = 4 * kSms;
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -79,11 +78,13 @@ size_t paged_ws_part(long long T, int group, int d, PagedShape v, int* rows_cap,
   return head + ml + round256(static_cast<size_t>(v.ctas) * 2 * cap * ((d + 3) / 4 * 4) * sizeof(float));
 }
 
-// CTAs of a CUDA-core variant: what shared memory lets an SM hold, up to four.
-PagedShape simt_shape(bool few, int d) {
-  const size_t smem = few ? fa::PagedSimtLayout<1, 4>::bytes(d) : fa::PagedSimtLayout<4, 1>::bytes(d);
-  const int per_sm = static_cast<int>(std::min<size_t>(4, 233472 / (smem + 1024)));
-  return {few ? 8 : 32, kSms * per_sm};
+// CTAs of a CUDA-core variant: what shared memory lets an SM hold, up to what its registers are
+// kept for.
+template <typename Shape>
+PagedShape simt_shape(int d) {
+  using L = fa::PagedSimtLayout<Shape>;
+  const int per_sm = static_cast<int>(std::min<size_t>(L::ctas((d + 31) / 32), 233472 / (L::bytes(d) + 1024)));
+  return {L::R, kSms * per_sm};
 }
 
 PagedShape decode_shape() { return {16, kSms}; }
@@ -91,7 +92,8 @@ PagedShape chunk_shape(int d) { return {256, kSms * (d == 64 ? fa::PagedChunkLay
 
 size_t paged_ws_bytes(long long T, int group, int d) {
   size_t n = 0;
-  for (const PagedShape v : {simt_shape(true, d), simt_shape(false, d), decode_shape(), chunk_shape(d)})
+  for (const PagedShape v : {simt_shape<fa::PagedSimtFew>(d), simt_shape<fa::PagedSimtChunk>(d), decode_shape(),
+                             chunk_shape(d)})
     n = std::max(n, paged_ws_part(T, group, d, v, nullptr, nullptr, nullptr));
   return n;
 }
@@ -131,17 +133,21 @@ void paged_tiles(fa::PagedParams& p, PagedShape v, int H_kv, void* ws) {
   p.ws_o = reinterpret_cast<float*>(b + off_o);
 }
 
-template <typename T, int WR, int WK>
+template <typename Shape>
 int launch_paged_simt(fa::PagedParams p, int H_kv, void* ws, cudaStream_t s) {
-  using L = fa::PagedSimtLayout<WR, WK>;
-  const PagedShape v = simt_shape(WK > 1, p.d);
+  using L = fa::PagedSimtLayout<Shape>;
+  const PagedShape v = simt_shape<Shape>(p.d);
   paged_tiles(p, v, H_kv, ws);
   const size_t smem = L::bytes(p.d);
-  int rc = set_smem(fa::fa_paged_simt_kernel<T, WR, WK>, static_cast<int>(smem));
+  void (*const kernels[4])(const fa::PagedParams) = {
+      fa::fa_paged_simt_kernel<Shape, 1>, fa::fa_paged_simt_kernel<Shape, 2>,
+      fa::fa_paged_simt_kernel<Shape, 3>, fa::fa_paged_simt_kernel<Shape, 4>};
+  auto* kern = kernels[(p.d - 1) / 32];
+  int rc = set_smem(kern, static_cast<int>(smem));
   if (rc != FA_OK) return rc;
-  fa::fa_paged_simt_kernel<T, WR, WK><<<v.ctas, 128, smem, s>>>(p);
+  kern<<<v.ctas, L::THREADS, smem, s>>>(p);
   if ((rc = check_launch("fa_paged_simt_kernel")) != FA_OK) return rc;
-  return launch_join<T>(p, v.ctas, WK > 1, s);
+  return launch_join<float>(p, v.ctas, Shape::WK > 1, s);
 }
 
 // 4-D view [page][H_kv][page_size][d] bf16 of a cache, 128-byte swizzled boxes of 64 columns and
@@ -509,8 +515,8 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
     return d == 64 ? launch_paged_chunk<64>(p, H_kv, page_size, workspace, s)
                    : launch_paged_chunk<128>(p, H_kv, page_size, workspace, s);
   }
-  return rows <= 8 ? launch_paged_simt<float, 1, 4>(p, H_kv, workspace, s)
-                   : launch_paged_simt<float, 4, 1>(p, H_kv, workspace, s);
+  return rows <= 8 ? launch_paged_simt<fa::PagedSimtFew>(p, H_kv, workspace, s)
+                   : launch_paged_simt<fa::PagedSimtChunk>(p, H_kv, workspace, s);
 }
 
 }  // extern "C"

@@ -1,30 +1,48 @@
 // fa_paged_simt.cuh -- paged attention on CUDA cores: fp32 inputs, fp32 products and sums.
 //
-// 128 threads; warps in WR row groups x WK key groups, 8 rows and 32 keys per warp and key
-// tile.  Lane = key for the scores (8 dot products per lane, Q rows broadcast from shared
-// memory), lane = four columns for P V.  K and V rows are padded so that 16-byte reads of 32
-// rows at one column spread over all banks.  K and V tiles come by 16-byte asynchronous copies,
-// the K tile of step t+1 while P V of step t runs and the V tile while the scores are formed.
-//   WR = 1, WK = 4 (8 rows, 128 keys a tile): few rows per K/V head (decoding).
-//   WR = 4, WK = 1 (32 rows, 32 keys a tile): chunks; each key is read once per 32 rows, where
-//   8 rows would make every SM read 64 bytes of L2 a cycle.
+// Warps in WR row groups x WK key groups, RW rows and 32 KPL keys per warp and key tile.  Lane =
+// key for the scores (RW dot products per key of the lane, as packed pairs of products, Q rows
+// broadcast from shared memory); for P V a lane has the columns lane, lane + 32, .. (NC of them,
+// the head dimension over 32 rounded up, so that a head of 64 or 80 columns does not pay for
+// 128).  K and V rows are padded so that 16-byte reads of 32 rows at one column spread over all
+// banks.  K and V tiles come by 16-byte asynchronous copies, the K tile of step t+1 while P V of
+// step t runs and the V tile while the scores are formed; the page of a key is looked up two
+// tiles ahead.  The reference maximum of a row moves only when a score exceeds it by more than 8
+// (in log2 units), which one vote finds; so most tiles need no reduction over lanes.
+//   PagedSimtFew (8 rows, 128 keys a tile, 8 warps): few rows per K/V head (decoding); bound by
+//     HBM, so many keys in flight and little to do per key.
+//   PagedSimtChunk (32 rows, 64 keys a tile, 4 warps): each key is read once per 32 rows, where 8
+//     rows would make every SM read 64 bytes of L2 a cycle.  Bound by FFMA and shared-memory
+//     reads, which two keys per lane balance: a Q row is read once for both.
 #pragma once
 #include "fa_paged.cuh"
 
 namespace fa {
 
-template <int WR, int WK>
+struct PagedSimtFew {
+  static constexpr int WR = 2, WK = 4, RW = 4, KPL = 1;
+};
+struct PagedSimtChunk {
+  static constexpr int WR = 4, WK = 1, RW = 8, KPL = 2;
+};
+
+template <typename Shape>
 struct PagedSimtLayout {
-  static constexpr int R = 8 * WR, KT = 32 * WK;
+  static constexpr int WARPS = Shape::WR * Shape::WK, THREADS = 32 * WARPS;
+  static constexpr int R = Shape::WR * Shape::RW, KT = 32 * Shape::WK * Shape::KPL;
   static constexpr int C = 1;  // an item's constant, in key tiles
+  static constexpr int P = 32 * Shape::KPL * Shape::RW;  // P of a warp, floats
+  static_assert(WARPS * Shape::RW <= KT, "the warps' sums fit the K tile");
+  static_assert(2 * WARPS * Shape::RW <= WARPS * P, "the warps' statistics fit P");
   // row pitch in floats of a d-column tile: an odd number of 16-byte chunks
   __host__ __device__ static int pitch(int d) { return (((d + 3) / 4) | 1) * 4; }
-  // Q [R], K [KT], V [KT] rows, P [4 warps][32 keys][8 rows], row offsets 2 x [KT]; the K and V
-  // tiles (KT * 2 * pitch floats) later hold the warps' sums [4][8][pitch] and statistics
+  // Q [R], K [KT], V [KT] rows, P [warps], offsets of the keys' rows in k and v [3 tiles][2][KT];
+  // the K tile later holds the warps' sums, P their statistics
   static size_t bytes(int d) {
-    return (static_cast<size_t>(R + 2 * KT) * pitch(d) + 4 * 32 * 8) * 4 + 2 * KT * 8 +
-           sizeof(PagedSched);
+    return (static_cast<size_t>(R + 2 * KT) * pitch(d) + WARPS * P) * 4 + 6 * KT * 8 + sizeof(PagedSched);
   }
+  // CTAs per SM that registers are kept for
+  __host__ __device__ static constexpr int ctas(int nc) { return Shape::WK > 1 ? (nc > 2 ? 1 : 2) : (nc == 4 ? 2 : 3); }
 };
 
 __device__ __forceinline__ void cp_async16(void* smem, const void* g) {
@@ -36,33 +54,37 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T, int WR, int WK>
-__global__ void __launch_bounds__(128) fa_paged_simt_kernel(const PagedParams p) {
-  using L = PagedSimtLayout<WR, WK>;
-  constexpr int R = L::R, KT = L::KT, RW = 8, C = L::C;
-  static_assert(WR * WK == 4, "four warps");
+template <typename Shape, int NC>
+__global__ void __launch_bounds__(PagedSimtLayout<Shape>::THREADS, PagedSimtLayout<Shape>::ctas(NC))
+fa_paged_simt_kernel(const PagedParams p) {
+  using L = PagedSimtLayout<Shape>;
+  constexpr int R = L::R, KT = L::KT, C = L::C, NT = L::THREADS;
+  constexpr int WK = Shape::WK, RW = Shape::RW, KPL = Shape::KPL;
   extern __shared__ __align__(16) uint8_t smem_simt[];
   const int d = p.d, pitch = L::pitch(d), dv = (d + 3) / 4;
   float* s_q = reinterpret_cast<float*>(smem_simt);
   float* s_k = s_q + R * pitch;
   float* s_v = s_k + KT * pitch;
-  float* s_p = s_v + KT * pitch;                                   // [4][32][8]
-  long long* s_off = reinterpret_cast<long long*>(s_p + 4 * 32 * 8);  // [2][KT]
-  PagedSched& sched = *reinterpret_cast<PagedSched*>(s_off + 2 * KT);
+  float* s_p = s_v + KT * pitch;
+  long long* s_off = reinterpret_cast<long long*>(s_p + L::WARPS * L::P);
+  PagedSched& sched = *reinterpret_cast<PagedSched*>(s_off + 6 * KT);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wr = warp / WK, wk = warp % WK;
   const int tpt = R / p.G;  // G <= R
 
   grid_dep_launch();
   // zero the columns that pad d up to a multiple of 4 (read by the 16-byte accesses)
-  for (int e = tid; e < (R + 2 * KT) * pitch; e += 128) s_q[e] = 0.f;
+  for (int e = tid; e < (R + 2 * KT) * pitch; e += NT) s_q[e] = 0.f;
   const int cta = blockIdx.x;
   long long x, hi;
-  if (!paged_share<KT, C, 128>(p, tpt, sched, x, hi)) return;
-  float* my_p = s_p + warp * 32 * 8;
+  if (!paged_share<KT, C, NT>(p, tpt, sched, x, hi)) return;
+  float* my_p = s_p + warp * L::P;
+  // this thread's first 16-byte chunk (or element) of a tile, and the step to its next
+  const int per_row = p.vec ? dv : d;
+  const int ld_r = tid / per_row, ld_c = tid % per_row, ld_dr = NT / per_row, ld_dc = NT % per_row;
 
   while (x < hi) {
-    paged_list<KT, C, 128>(p, tpt, x, hi, sched);
+    paged_list<KT, C, NT>(p, tpt, x, hi, sched);
     PagedPieces<C> pieces;
     pieces.start(p, sched, x);
     PagedPiece pc;
@@ -72,134 +94,153 @@ __global__ void __launch_bounds__(128) fa_paged_simt_kernel(const PagedParams p)
       const int keys = paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok);
       const int32_t* table = p.table + rc.b * p.table_stride;
       const long long hrow = static_cast<long long>(pc.h / p.splits) << p.page_shift;
-      // page << 32 | row within the page's heads, or -1: no such key
-      auto row_offsets = [&](int t, int buf) {
-        for (int e = tid; e < KT; e += 128) {
-          const int j = t * KT + e;
-          long long o = -1;
-          if (j < keys) {
-            const int pg = table[j >> p.page_shift];
-            if (pg >= 0 && pg < p.num_pages)
-              o = (static_cast<long long>(pg) << 32) |
-                  static_cast<long long>((hrow + (j & ((1 << p.page_shift) - 1))));
-          }
-          s_off[buf * KT + e] = o;
-        }
+      // key tid of tile t: its page (-1: no such key, or the table does not name one) ...
+      auto page_of = [&](int t) -> int {
+        const int j = t * KT + tid;
+        if (tid >= KT || j >= keys) return -1;
+        return table[j >> p.page_shift];
+      };
+      // ... and, noted for the copies, where its rows start in k and v, or -1
+      auto note = [&](int t, int pg) {
+        if (tid >= KT) return;
+        const bool there = pg >= 0 && pg < p.num_pages;
+        const long long row = (hrow + ((t * KT + tid) & ((1 << p.page_shift) - 1))) * d;
+        s_off[t % 3 * 2 * KT + tid] = there ? pg * p.k_page + row : -1;
+        s_off[t % 3 * 2 * KT + KT + tid] = there ? pg * p.v_page + row : -1;
       };
       // missing keys become zero rows: a stale row may hold anything, and 0 times it is not 0
-      auto load = [&](float* dst, const void* base, long long page_stride, int buf) {
-        const long long* off = s_off + buf * KT;
-        const T* g = static_cast<const T*>(base);
-        if (sizeof(T) == 4 && p.vec) {
-          for (int e = tid; e < KT * dv; e += 128) {
-            const int r = e / dv, c = (e - r * dv) * 4;
-            const long long o = off[r];
-            if (o >= 0)
-              cp_async16(dst + r * pitch + c, g + (o >> 32) * page_stride + (o & 0xffffffffll) * d + c);
-            else
-              *reinterpret_cast<float4*>(dst + r * pitch + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto load = [&](float* dst, const void* base, const long long* off) {
+        const float* g = static_cast<const float*>(base);
+        for (int r = ld_r, c = ld_c; r < KT;) {
+          const long long o = off[r];
+          if (p.vec) {
+            if (o >= 0) cp_async16(dst + r * pitch + 4 * c, g + o + 4 * c);
+            else *reinterpret_cast<float4*>(dst + r * pitch + 4 * c) = make_float4(0.f, 0.f, 0.f, 0.f);
+          } else {
+            dst[r * pitch + c] = o >= 0 ? g[o + c] : 0.f;
           }
-        } else {
-          for (int e = tid; e < KT * d; e += 128) {
-            const int r = e / d, c = e - r * d;
-            const long long o = off[r];
-            dst[r * pitch + c] =
-                o >= 0 ? to_f<T>(g[(o >> 32) * page_stride + (o & 0xffffffffll) * d + c]) : 0.f;
+          r += ld_dr;
+          c += ld_dc;
+          if (c >= per_row) {
+            c -= per_row;
+            ++r;
           }
         }
         cp_async_commit();
       };
+      auto load_k = [&](int t) { load(s_k, p.k, s_off + t % 3 * 2 * KT); };
+      auto load_v = [&](int t) { load(s_v, p.v, s_off + t % 3 * 2 * KT + KT); };
       __syncthreads();  // the previous piece's reads of every shared array are over
-      for (int e = tid; e < R * d; e += 128) {
+      for (int e = tid; e < R * d; e += NT) {
         const int r = e / d, c = e - r * d;
         const long long tok = rc.tok0 + r / p.G;
         const int qh = paged_row_head(p, pc.h, r, rows);
         s_q[r * pitch + c] =
-            qh >= 0 ? to_f<T>(static_cast<const T*>(p.q)[tok * p.q_st + qh * p.q_sh + c]) : 0.f;
+            qh >= 0 ? static_cast<const float*>(p.q)[tok * p.q_st + qh * p.q_sh + c] : 0.f;
       }
-      row_offsets(pc.a, pc.a & 1);
+      note(pc.a, page_of(pc.a));
+      if (pc.a + 1 < pc.b) note(pc.a + 1, page_of(pc.a + 1));
       __syncthreads();
-      load(s_k, p.k, p.k_page, pc.a & 1);
-      load(s_v, p.v, p.v_page, pc.a & 1);
+      load_k(pc.a);
+      load_v(pc.a);
 
-      float m[RW], l[RW], acc[RW][4];
+      float m[RW], l[RW], acc[RW][NC];
       int lim[RW];  // last key that the row sees
 #pragma unroll
       for (int r = 0; r < RW; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
-        acc[r][0] = acc[r][1] = acc[r][2] = acc[r][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[r][c] = 0.f;
         const int tok = (wr * RW + r) / p.G;
         lim[r] = p.causal ? rc.pos0 + tok : 0x7fffffff;
       }
       const float* q0 = s_q + wr * RW * pitch;
+      const int key0 = wk * 32 * KPL;  // the warp's first key of a tile; the lane's: key0 + 32 k + lane
       for (int t = pc.a; t < pc.b; ++t) {
-        const int buf = t & 1;
+        const int pg_next = t + 2 < pc.b ? page_of(t + 2) : -1;
         cp_async_wait<1>();
         __syncthreads();  // K of this tile is in
-        // ---- scores of key wk * 32 + lane
-        const float* kr = s_k + (wk * 32 + lane) * pitch;
-        float s[RW];
+        const float* kr = s_k + (key0 + lane) * pitch;
+        float sa[KPL][RW], sb[KPL][RW];  // sums of the even and the odd products
 #pragma unroll
-        for (int r = 0; r < RW; ++r) s[r] = 0.f;
+        for (int k = 0; k < KPL; ++k)
+#pragma unroll
+          for (int r = 0; r < RW; ++r) sa[k][r] = sb[k][r] = 0.f;
         for (int c = 0; c < 4 * dv; c += 4) {
-          const float4 kv = *reinterpret_cast<const float4*>(kr + c);
+          float4 kv[KPL];
+#pragma unroll
+          for (int k = 0; k < KPL; ++k) kv[k] = *reinterpret_cast<const float4*>(kr + 32 * k * pitch + c);
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
             const float4 qv = *reinterpret_cast<const float4*>(q0 + r * pitch + c);
-            s[r] = fmaf(qv.x, kv.x, s[r]);
-            s[r] = fmaf(qv.y, kv.y, s[r]);
-            s[r] = fmaf(qv.z, kv.z, s[r]);
-            s[r] = fmaf(qv.w, kv.w, s[r]);
+#pragma unroll
+            for (int k = 0; k < KPL; ++k) {
+              ffma2(sa[k][r], sb[k][r], qv.x, qv.y, kv[k].x, kv[k].y, sa[k][r], sb[k][r]);
+              ffma2(sa[k][r], sb[k][r], qv.z, qv.w, kv[k].z, kv[k].w, sa[k][r], sb[k][r]);
+            }
           }
         }
-        const int j = t * KT + wk * 32 + lane;
-        const bool there = s_off[buf * KT + wk * 32 + lane] >= 0;
+        bool there[KPL];
+#pragma unroll
+        for (int k = 0; k < KPL; ++k) there[k] = s_off[t % 3 * 2 * KT + key0 + 32 * k + lane] >= 0;
+        const int j = t * KT + key0 + lane;
 #pragma unroll
         for (int r = 0; r < RW; ++r) {
-          const float v = (there && j <= lim[r]) ? s[r] * p.scale2 : -INFINITY;
-          float mx = v;
+          float top = -INFINITY;
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const float mn = fmaxf(m[r], mx);
-          const float pe = v == -INFINITY ? 0.f : exp2f(v - mn);
-          if (mn != m[r]) {  // the same for the whole warp
+          for (int k = 0; k < KPL; ++k) {
+            sa[k][r] = (there[k] && j + 32 * k <= lim[r]) ? (sa[k][r] + sb[k][r]) * p.scale2 : -INFINITY;
+            top = fmaxf(top, sa[k][r]);
+          }
+          if (__any_sync(0xffffffffu, top > m[r] + 8.0f)) {
+            float mn = fmaxf(m[r], top);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
             const float a = exp2f(m[r] - mn);
             l[r] *= a;
-            acc[r][0] *= a;
-            acc[r][1] *= a;
-            acc[r][2] *= a;
-            acc[r][3] *= a;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) acc[r][c] *= a;
             m[r] = mn;
           }
-          l[r] += pe;
-          my_p[lane * 8 + r] = pe;
+#pragma unroll
+          for (int k = 0; k < KPL; ++k) {
+            sa[k][r] = sa[k][r] == -INFINITY ? 0.f : exp2f(sa[k][r] - m[r]);
+            l[r] += sa[k][r];
+          }
         }
-        if (t + 1 < pc.b) row_offsets(t + 1, buf ^ 1);
-        __syncthreads();  // K read, P written, the next row offsets known
-        if (t + 1 < pc.b) load(s_k, p.k, p.k_page, buf ^ 1);
+#pragma unroll
+        for (int k = 0; k < KPL; ++k)
+#pragma unroll
+          for (int r = 0; r < RW; r += 4)
+            *reinterpret_cast<float4*>(my_p + (32 * k + lane) * RW + r) =
+                make_float4(sa[k][r], sa[k][r + 1], sa[k][r + 2], sa[k][r + 3]);
+        if (t + 2 < pc.b) note(t + 2, pg_next);
+        __syncthreads();  // K read, P written
+        if (t + 1 < pc.b) load_k(t + 1);
         else cp_async_commit();
         cp_async_wait<1>();
         __syncthreads();  // V of this tile is in
-        if (lane < dv) {
-          const float* vr = s_v + wk * 32 * pitch + lane * 4;
+        const float* vr = s_v + key0 * pitch + lane;
 #pragma unroll 4
-          for (int kk = 0; kk < 32; ++kk) {
-            const float4 vv = *reinterpret_cast<const float4*>(vr + kk * pitch);
-            const float4 pa = *reinterpret_cast<const float4*>(my_p + kk * 8);
-            const float4 pb = *reinterpret_cast<const float4*>(my_p + kk * 8 + 4);
-            const float pr[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+        for (int kk = 0; kk < 32 * KPL; ++kk) {
+          float vv[NC];
 #pragma unroll
-            for (int r = 0; r < RW; ++r) {
-              acc[r][0] = fmaf(pr[r], vv.x, acc[r][0]);
-              acc[r][1] = fmaf(pr[r], vv.y, acc[r][1]);
-              acc[r][2] = fmaf(pr[r], vv.z, acc[r][2]);
-              acc[r][3] = fmaf(pr[r], vv.w, acc[r][3]);
+          for (int c = 0; c < NC; ++c) vv[c] = 32 * c + lane < 4 * dv ? vr[kk * pitch + 32 * c] : 0.f;
+#pragma unroll
+          for (int r = 0; r < RW; r += 4) {
+            const float4 pr = *reinterpret_cast<const float4*>(my_p + kk * RW + r);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              acc[r][c] = fmaf(pr.x, vv[c], acc[r][c]);
+              acc[r + 1][c] = fmaf(pr.y, vv[c], acc[r + 1][c]);
+              acc[r + 2][c] = fmaf(pr.z, vv[c], acc[r + 2][c]);
+              acc[r + 3][c] = fmaf(pr.w, vv[c], acc[r + 3][c]);
             }
           }
         }
         __syncthreads();  // V and P read
-        if (t + 1 < pc.b) load(s_v, p.v, p.v_page, buf ^ 1);
+        if (t + 1 < pc.b) load_v(t + 1);
         else cp_async_commit();
       }
       cp_async_wait<0>();
@@ -208,74 +249,55 @@ __global__ void __launch_bounds__(128) fa_paged_simt_kernel(const PagedParams p)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
 
-      // ---- join the key groups (WK > 1) through the K tile's memory, then write
-      float* s_ml = s_p;  // [4 warps][8 rows] (m, l)
-      if (WK > 1) {
+      const bool whole = pc.a == 0 && pc.b == rc.n;
+      const size_t slot = paged_slot(cta, pc);
+      auto write = [&](int r, float mm, float ll, const float (&o)[NC]) {
+        const int qh = paged_row_head(p, pc.h, r, rows);
+        if (qh < 0) return;
+        const float f = !whole ? 1.0f : (ll == 0.f ? 0.0f : 1.0f / ll);
+        const long long row = static_cast<long long>(rc.tok0 + r / p.G) * p.H + qh;
+        float* op = whole ? static_cast<float*>(p.o) + row * d : p.ws_o + (slot * p.rows_cap + r) * p.ws_pitch;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          if (32 * c + lane < d) op[32 * c + lane] = o[c] * f;
+        if (lane == 0) {
+          if (whole) p.lse[row] = paged_lse(mm, ll);
+          else p.ws_ml[slot * p.rows_cap + r] = make_float2(mm, ll);
+        }
+      };
+      if constexpr (WK == 1) {
+#pragma unroll
+        for (int r = 0; r < RW; ++r) write(wr * RW + r, m[r], l[r], acc[r]);
+      } else {
+        // join the key groups: their sums through the K tile's memory, statistics through P's
+        float2* s_ml = reinterpret_cast<float2*>(s_p);  // [warps][RW]
         if (lane == 0)
-          for (int r = 0; r < RW; ++r) {
-            s_ml[(warp * 8 + r) * 2] = m[r];
-            s_ml[(warp * 8 + r) * 2 + 1] = l[r];
-          }
+          for (int r = 0; r < RW; ++r) s_ml[warp * RW + r] = make_float2(m[r], l[r]);
         __syncthreads();
-        float* so = s_k + warp * 8 * pitch;
 #pragma unroll
         for (int r = 0; r < RW; ++r) {
           float mm = -INFINITY;
-          for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_ml[(w * 8 + r) * 2]);
+          for (int w = 0; w < WK; ++w) mm = fmaxf(mm, s_ml[(wr * WK + w) * RW + r].x);
           const float a = m[r] == -INFINITY ? 0.f : exp2f(m[r] - mm);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)  // never the padding columns, which stay zero
-            if (lane * 4 + c < d) so[r * pitch + lane * 4 + c] = acc[r][c] * a;
+          for (int c = 0; c < NC; ++c)  // never the padding columns, which stay zero
+            if (32 * c + lane < d) s_k[(warp * RW + r) * pitch + 32 * c + lane] = acc[r][c] * a;
         }
         __syncthreads();
-      }
-      const bool whole = pc.a == 0 && pc.b == rc.n;
-      const size_t slot = paged_slot(cta, pc);
+        for (int r = warp; r < R; r += L::WARPS) {
+          const int first = r / RW * WK, in = r % RW;  // the row's warps, its row in them
+          float mm = -INFINITY, ll = 0.f, o[NC];
+          for (int w = 0; w < WK; ++w) mm = fmaxf(mm, s_ml[(first + w) * RW + in].x);
 #pragma unroll
-      for (int rr = 0; rr < (WK > 1 ? 2 : RW); ++rr) {
-        // WK > 1: warp w finishes rows 2w, 2w+1; else each warp its own 8
-        const int r = WK > 1 ? 2 * warp + rr : wr * RW + rr;
-        const int qh = paged_row_head(p, pc.h, r, rows);
-        if (qh < 0) continue;
-        float mm, ll;
-        float4 o4;
-        if constexpr (WK > 1) {
-          mm = -INFINITY;
-          for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_ml[(w * 8 + r) * 2]);
-          ll = 0.f;
-          o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int w = 0; w < 4; ++w) {
-            const float mw = s_ml[(w * 8 + r) * 2];
-            if (mw != -INFINITY) ll = fmaf(s_ml[(w * 8 + r) * 2 + 1], exp2f(mw - mm), ll);
-            if (lane < dv) {
-              const float4 a4 = *reinterpret_cast<const float4*>(s_k + (w * 8 + r) * pitch + lane * 4);
-              o4.x += a4.x;
-              o4.y += a4.y;
-              o4.z += a4.z;
-              o4.w += a4.w;
-            }
+          for (int c = 0; c < NC; ++c) o[c] = 0.f;
+          for (int w = 0; w < WK; ++w) {
+            const float2 ml = s_ml[(first + w) * RW + in];
+            if (ml.x != -INFINITY) ll = fmaf(ml.y, exp2f(ml.x - mm), ll);
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (32 * c + lane < d) o[c] += s_k[((first + w) * RW + in) * pitch + 32 * c + lane];
           }
-        } else {
-          mm = m[rr];
-          ll = l[rr];
-          o4 = make_float4(acc[rr][0], acc[rr][1], acc[rr][2], acc[rr][3]);
-        }
-        if (whole) {
-          const float inv = ll == 0.f ? 0.0f : 1.0f / ll;
-          const long long row = static_cast<long long>(rc.tok0 + r / p.G) * p.H + qh;
-          T* op = static_cast<T*>(p.o) + row * d;
-          const float ov[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (lane * 4 + c < d) op[lane * 4 + c] = from_f<T>(ov[c] * inv);
-          if (lane == 0) p.lse[row] = paged_lse(mm, ll);
-        } else {
-          float* op = p.ws_o + (slot * p.rows_cap + r) * p.ws_pitch;
-          const float ov[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (lane * 4 + c < d) op[lane * 4 + c] = ov[c];
-          if (lane == 0) p.ws_ml[slot * p.rows_cap + r] = make_float2(mm, ll);
+          write(r, mm, ll, o);
         }
       }
       if (tid == 0 && pc.a == 0 && pc.b < rc.n) paged_header<C>(p, sched, rc, pc.h, cta);
