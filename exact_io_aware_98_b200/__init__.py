@@ -8,9 +8,9 @@ library is missing or no GPU is present, every call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -48,6 +48,10 @@ SIGNATURES = {
     "fa_paged_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_paged_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _l, _l, _l,
                           _l, _l, _i, _i, _i, _i, _f, _i, _i, _vp, _sz, _vp]),
+    "fa_rope_packed": (_i, [ctypes.c_char_p]),
+    "fa_paged_plan_packed": (_i, [ctypes.c_char_p]),
+    "fa_paged_append_packed": (_i, [ctypes.c_char_p]),
+    "fa_paged_fwd_packed": (_i, [ctypes.c_char_p]),
     "fa_fwd_tile_reference": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp,
                                    _i, _i, _vp]),
     "fa_naive_workspace_size": (_sz, [_i, _i, _i]),
@@ -267,7 +271,12 @@ ROPE_INTERLEAVED, ROPE_BACKWARD = 1, 2   # fa.h FA_ROPE_*
 
 # The calls below are a few microseconds of GPU work at a decoding step's sizes, so their checks are
 # written for the host: device numbers, shapes and dtypes are compared directly, and only a
-# comparison that fails goes through the functions that say which.
+# comparison that fails goes through the functions that say which.  The arguments go over in one
+# packed structure (fa.h, fa_*_args), which costs a third of what as many ctypes arguments do.
+_ROPE = struct.Struct("@Q5Q7q7if")
+_PLAN = struct.Struct("@Q11Qq6i")
+_APPEND = struct.Struct("@Q10Q10q9if")
+_FWD = struct.Struct("@Q11Q5q11if")
 
 
 def _refuse(dev: int, *specs):
@@ -288,19 +297,21 @@ def _refuse(dev: int, *specs):
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent without CUDA
 _get_device = getattr(torch._C, "_cuda_getDevice", None)
-_strides3 = functools.lru_cache(maxsize=4096)(lambda *x: (_l * 3)(*x))
-_strides8 = functools.lru_cache(maxsize=4096)(lambda *x: (_l * 8)(*x))
 
 
-def _call(dev: int, fn, *args):
-    """One library call on CUDA device ``dev``'s current stream, whatever device is current."""
+def _call(dev: int, fn, args: struct.Struct, *values):
+    """One packed call with CUDA device ``dev`` current; its stream is among the values."""
+    try:
+        packed = args.pack(args.size, *values)
+    except (struct.error, OverflowError) as e:  # a size that is no int32, a scale that is no float
+        raise FaError(f"{fn.__name__.removesuffix('_packed')}: {e}") from None
     if dev == _get_device():
-        rc = fn(*args, _raw_stream(dev))
+        rc = fn(packed)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev))
+            rc = fn(packed)
     if rc != 0:
-        _check(rc, fn.__name__)
+        _check(rc, fn.__name__.removesuffix("_packed"))
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
@@ -353,15 +364,14 @@ def _rope(x, inv_freq, positions, interleaved, magnitude, out, options):
     if len(shape) == 3:
         N, H, d = shape
         B = 1
-        xa, ya = _strides3(0, xs[1], xs[0]), _strides3(0, ys[1], ys[0])
+        xs, ys = (0, xs[1], xs[0], xs[2]), (0, ys[1], ys[0], ys[2])
     elif len(shape) == 4:
         B, H, N, d = shape
-        xa, ya = _strides3(*xs[:3]), _strides3(*ys[:3])
     else:
         raise FaError(f"x must be [B, H, N, d] or [T, H, d], got {tuple(shape)}")
     if d > 1 and (xs[-1] != 1 or ys[-1] != 1):
         raise FaError("the last dimension of x and out must be contiguous")
-    ps, pp = 0, None
+    ps = pp = 0
     if positions is not None:
         if positions.get_device() != dev or positions.dtype is not torch.int32:
             _refuse(dev, ("positions", positions, torch.int32, None, False))
@@ -372,9 +382,9 @@ def _rope(x, inv_freq, positions, interleaved, magnitude, out, options):
         if N > 1 and positions.stride(-1) != 1:
             raise FaError("positions must be contiguous along the tokens")
         pp = positions.data_ptr()
-    _call(dev, lib.fa_rope, x.data_ptr(), y.data_ptr(), pp, inv_freq.data_ptr(), B, H, N, d,
-          2 * inv_freq.numel(), xa, ya, ps, float(magnitude),
-          options | ROPE_INTERLEAVED if interleaved else options, _dtype_code(x))
+    _call(dev, lib.fa_rope_packed, _ROPE, x.data_ptr(), y.data_ptr(), pp, inv_freq.data_ptr(), _raw_stream(dev),
+          xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], ps, B, H, N, d, 2 * inv_freq.numel(),
+          options | ROPE_INTERLEAVED if interleaved else options, _dtype_code(x), magnitude)
     return y
 
 
@@ -440,15 +450,15 @@ def paged_plan(ctx_len, new_len, free_pages, block_table, page_size: int, max_to
     ts, stride = block_table.shape, block_table.stride()
     if len(ts) != 2 or ts[0] != B or ts[1] < 1 or (ts[1] > 1 and stride[1] != 1):
         raise FaError(f"block_table must be [{B}, max_pages] with contiguous rows")
-    cp = None
+    cp = 0
     if cursor is not None:
         _refuse(dev, ("cursor", cursor, i32, None, True))
         if cursor.numel() != 1:
             raise FaError("cursor must hold one number")
         cp = cursor.data_ptr()
-    _call(dev, lib.fa_paged_plan, ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(),
-          free_pages.numel(), cp, block_table.data_ptr(), stride[0], B, ts[1], int(page_size), max_tokens,
-          cu_q.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), slots.data_ptr(), counts.data_ptr())
+    _call(dev, lib.fa_paged_plan_packed, _PLAN, ctx_len.data_ptr(), new_len.data_ptr(), free_pages.data_ptr(), cp,
+          block_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), positions.data_ptr(), counts.data_ptr(),
+          slots.data_ptr(), _raw_stream(dev), stride[0], free_pages.numel(), B, ts[1], page_size, max_tokens, 0)
     return out
 
 
@@ -488,7 +498,7 @@ def paged_append(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None,
         raise FaError(f"k {tuple(shape)} and v must both be [T, H_kv, d]")
     T, H_kv, d = shape
     pages, page, k_page, v_page = _cache(dev, k_cache, v_cache, dtype, H_kv, d)
-    rot, pp, fp = 0, None, None
+    rot = pp = fp = 0
     if inv_freq is not None:
         if positions is None:
             raise FaError("inv_freq needs positions")
@@ -499,7 +509,7 @@ def paged_append(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None,
                     ("positions", positions, torch.int32, (T,), True))
         rot, pp, fp = 2 * inv_freq.numel(), positions.data_ptr(), inv_freq.data_ptr()
     ks, vs = k.stride(), v.stride()
-    H, qp, qop, qs, qos = 0, None, None, (0, 0, 1), (0, 0, 1)
+    H, qp, qop, qs, qos = 0, 0, 0, (0, 0, 1), (0, 0, 1)
     if q is not None:
         qshape = q.shape
         if q_out is None:
@@ -514,10 +524,10 @@ def paged_append(k, v, k_cache, v_cache, slots, positions=None, inv_freq=None,
         raise FaError("q_out without q")
     if d > 1 and (qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or qos[2] != 1):
         raise FaError("the last dimension of q, k, v and q_out must be contiguous")
-    _call(dev, lib.fa_paged_append, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
-          v_cache.data_ptr(), slots.data_ptr(), pp, fp, T, H, H_kv, d, rot,
-          _strides8(qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qos[0], qos[1]), k_page, v_page, page,
-          pages, float(magnitude), ROPE_INTERLEAVED if interleaved else 0, _dtype_code(k))
+    _call(dev, lib.fa_paged_append_packed, _APPEND, qp, k.data_ptr(), v.data_ptr(), qop, k_cache.data_ptr(),
+          v_cache.data_ptr(), slots.data_ptr(), pp, fp, _raw_stream(dev), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1],
+          qos[0], qos[1], k_page, v_page, T, H, H_kv, d, rot, page, pages,
+          ROPE_INTERLEAVED if interleaved else 0, _dtype_code(k), magnitude)
     return q_out
 
 
@@ -566,12 +576,11 @@ def paged_fwd(q, k_cache, v_cache, block_table, kv_len, cu_q, scale: Optional[fl
         _refuse(dev, ("kv_len", kv_len, i32, (B,), True), ("cu_q", cu_q, i32, (B + 1,), True),
                 ("block_table", block_table, i32, None, False), ("out", out, dtype, shape, True),
                 ("lse", lse, torch.float32, shape[:2], True), ("workspace", workspace, torch.uint8, None, True))
-    _call(dev, lib.fa_paged_fwd, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _call(dev, lib.fa_paged_fwd_packed, _FWD, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           block_table.data_ptr(), kv_len.data_ptr(), cu_q.data_ptr(), out.data_ptr(), lse.data_ptr(),
-          T, B, H, H_kv, d, qs[0], qs[1], k_page, v_page, stride[0], page, pages, ts[1],
-          0 if max_q is None else int(max_q), default_scale(d) if scale is None else float(scale),
-          1 if causal else 0,
-          _dtype_code(q), workspace.data_ptr(), workspace.numel())
+          workspace.data_ptr(), _raw_stream(dev), workspace.numel(), qs[0], qs[1], k_page, v_page, stride[0], T, B,
+          H, H_kv, d, page, pages, ts[1], 0 if max_q is None else max_q, 1 if causal else 0, _dtype_code(q),
+          default_scale(d) if scale is None else scale)
     return out, lse
 
 

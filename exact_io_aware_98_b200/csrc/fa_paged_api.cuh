@@ -232,6 +232,18 @@ int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cud
   return launch_join<__nv_bfloat16>(p, v.ctas, false, s);
 }
 
+// Copies a packed call's arguments (which need not be aligned) after checking their size.
+template <typename Args>
+int unpack(const Args* packed, Args* a) {
+  if (packed == nullptr) return fail(FA_ERR_INVALID, "null arguments");
+  std::memcpy(&a->size, packed, sizeof(a->size));
+  if (a->size != sizeof(Args))
+    return fail(FA_ERR_INVALID, "packed arguments of %llu bytes, not %zu",
+                static_cast<unsigned long long>(a->size), sizeof(Args));
+  std::memcpy(a, packed, sizeof(Args));
+  return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -517,6 +529,43 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
   }
   return rows <= 8 ? launch_paged_simt<fa::PagedSimtFew>(p, H_kv, workspace, s)
                    : launch_paged_simt<fa::PagedSimtChunk>(p, H_kv, workspace, s);
+}
+
+int fa_rope_packed(const fa_rope_args* args) {
+  fa_rope_args a;
+  const int rc = unpack(args, &a);
+  if (rc != FA_OK) return rc;
+  return fa_rope(a.x, a.y, a.positions, a.inv_freq, a.B, a.H, a.N, a.d, a.rotary_dim, a.x_strides,
+                 a.y_strides, a.positions_stride, a.magnitude, a.options, a.dtype, a.stream);
+}
+
+int fa_paged_plan_packed(const fa_paged_plan_args* args) {
+  fa_paged_plan_args a;
+  const int rc = unpack(args, &a);
+  if (rc != FA_OK) return rc;
+  return fa_paged_plan(a.ctx_len, a.new_len, a.free_pages, a.n_free, a.cursor, a.block_table,
+                       a.table_stride, a.B, a.max_pages, a.page_size, a.max_tokens, a.cu_q, a.kv_len,
+                       a.positions, a.slots, a.counts, a.stream);
+}
+
+int fa_paged_append_packed(const fa_paged_append_args* args) {
+  fa_paged_append_args a;
+  const int rc = unpack(args, &a);
+  if (rc != FA_OK) return rc;
+  return fa_paged_append(a.q, a.k, a.v, a.q_out, a.k_cache, a.v_cache, a.slots, a.positions,
+                         a.inv_freq, a.T, a.H, a.H_kv, a.d, a.rotary_dim, a.strides,
+                         a.k_page_stride, a.v_page_stride, a.page_size, a.num_pages, a.magnitude,
+                         a.options, a.dtype, a.stream);
+}
+
+int fa_paged_fwd_packed(const fa_paged_fwd_args* args) {
+  fa_paged_fwd_args a;
+  const int rc = unpack(args, &a);
+  if (rc != FA_OK) return rc;
+  return fa_paged_fwd(a.q, a.k_cache, a.v_cache, a.block_table, a.kv_len, a.cu_q, a.o, a.lse, a.T,
+                      a.B, a.H, a.H_kv, a.d, a.q_token_stride, a.q_head_stride, a.k_page_stride,
+                      a.v_page_stride, a.table_stride, a.page_size, a.num_pages, a.max_pages, a.max_q,
+                      a.scale, a.causal, a.dtype, a.workspace, a.workspace_bytes, a.stream);
 }
 
 }  // extern "C"

@@ -188,7 +188,7 @@ __device__ __forceinline__ void rope_block(const RopeShape& sh, int N, int n_hea
 #pragma unroll
     for (int k = 0; k < ROPE_DEPTH; ++k) {
       const int hk = h + k * sh.hs;
-      if (active && hk < h_end && rows.stored(hk)) {
+      if (active && hk < h_end) {  // a row that is not stored is read all the same: no wait for its slot
         const T* src = rows.src(hk);
         va[k].load(src + c0);
         if (c1 >= 0) vb[k].load(src + c1);

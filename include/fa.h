@@ -282,6 +282,61 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
                  float scale, int causal, int dtype, void* workspace, size_t workspace_bytes,
                  void* stream);
 
+/*
+ * Packed forms of the rotary and paged entry points: the same calls with their arguments in one
+ * structure, for bindings whose foreign-function layer costs time per argument (a decoding step's
+ * call is a few microseconds of GPU work).  The fields are the call's parameters in order, arrays
+ * of strides in place; `size` is the structure's size in bytes (another value: FA_ERR_INVALID).
+ */
+typedef struct {
+  uint64_t size;
+  const void* x;
+  void* y;
+  const int32_t* positions;
+  const double* inv_freq;
+  void* stream;
+  int64_t x_strides[3], y_strides[3], positions_stride;
+  int32_t B, H, N, d, rotary_dim, options, dtype;
+  float magnitude;
+} fa_rope_args;
+typedef struct {
+  uint64_t size;
+  const int32_t *ctx_len, *new_len, *free_pages, *cursor;
+  int32_t *block_table, *cu_q, *kv_len, *positions, *counts;
+  int64_t* slots;
+  void* stream;
+  int64_t table_stride;
+  int32_t n_free, B, max_pages, page_size, max_tokens, reserved;
+} fa_paged_plan_args;
+typedef struct {
+  uint64_t size;
+  const void *q, *k, *v;
+  void *q_out, *k_cache, *v_cache;
+  const int64_t* slots;
+  const int32_t* positions;
+  const double* inv_freq;
+  void* stream;
+  int64_t strides[8], k_page_stride, v_page_stride;
+  int32_t T, H, H_kv, d, rotary_dim, page_size, num_pages, options, dtype;
+  float magnitude;
+} fa_paged_append_args;
+typedef struct {
+  uint64_t size;
+  const void *q, *k_cache, *v_cache;
+  const int32_t *block_table, *kv_len, *cu_q;
+  void* o;
+  float* lse;
+  void *workspace, *stream;
+  uint64_t workspace_bytes;
+  int64_t q_token_stride, q_head_stride, k_page_stride, v_page_stride, table_stride;
+  int32_t T, B, H, H_kv, d, page_size, num_pages, max_pages, max_q, causal, dtype;
+  float scale;
+} fa_paged_fwd_args;
+int fa_rope_packed(const fa_rope_args* args);
+int fa_paged_plan_packed(const fa_paged_plan_args* args);
+int fa_paged_append_packed(const fa_paged_append_args* args);
+int fa_paged_fwd_packed(const fa_paged_fwd_args* args);
+
 /* Flags of fa_fwd_tile_reference: the other two axes of the deviation study. */
 enum {
   FA_TILE_REVERSE = 1,    /* visit the key tiles from the last to the first */

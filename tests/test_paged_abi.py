@@ -123,3 +123,39 @@ def test_binding_constants_match_the_header():
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "fa.h")).read()
     vals = {k: int(v) for k, v in re.findall(r"\b(FA_ROPE_[A-Z]+)\s*=\s*(\d+)", text)}
     assert vals == {"FA_ROPE_INTERLEAVED": fa.ROPE_INTERLEAVED, "FA_ROPE_BACKWARD": fa.ROPE_BACKWARD}
+
+
+def test_packed_calls(lib):
+    """The packed forms refuse what their calls refuse, and a structure of another size."""
+    A64 = A
+    rope = [A64, A64 + 4096, 0, A64, 0, 512, 256, 64, 512, 256, 64, 0, 1, 2, 4, 64, 64, 0, 0, 1.0]
+    plan = [A64, A64, A64, 0, A64, A64, A64, A64, A64, A64, 0, 8, 4, 2, 8, 16, 4, 0]
+    append = [A64, A64, A64, A64 + 4096, A64, A64, A64, A64, A64, 0, 128, 64, 64, 64, 64, 64, 128, 64, 1024, 1024,
+              2, 2, 1, 64, 64, 16, 4, 0, 0, 1.0]
+    fwd = [A64, A64, A64, A64, A64, A64, A64, A64, A64, 0, 1 << 30, 256, 64, 2048, 2048, 8, 4, 2, 4, 2, 64, 16, 4, 8, 1,
+           1, 0, 0.125]
+    for fn, st, ok, at, bad, code in (
+            (lib.fa_rope_packed, fa._ROPE, rope, 16, 63, INVALID), (lib.fa_rope_packed, fa._ROPE, rope, 0, A + 1, ALIGN),
+            (lib.fa_rope_packed, fa._ROPE, rope, 19, float("nan"), INVALID),
+            (lib.fa_rope_packed, fa._ROPE, rope, 14, 1 << 25, UNSUPPORTED),
+            (lib.fa_paged_plan_packed, fa._PLAN, plan, 15, 24, INVALID),
+            (lib.fa_paged_plan_packed, fa._PLAN, plan, 16, 0, INVALID),
+            (lib.fa_paged_plan_packed, fa._PLAN, plan, 9, A + 4, ALIGN),
+            (lib.fa_paged_append_packed, fa._APPEND, append, 23, 2048, UNSUPPORTED),
+            (lib.fa_paged_append_packed, fa._APPEND, append, 28, 2, INVALID),
+            (lib.fa_paged_append_packed, fa._APPEND, append, 6, A + 4, ALIGN),
+            (lib.fa_paged_append_packed, fa._APPEND, append, 29, float("inf"), INVALID),
+            (lib.fa_paged_fwd_packed, fa._FWD, fwd, 27, 0.0, INVALID),
+            (lib.fa_paged_fwd_packed, fa._FWD, fwd, 20, 96, UNSUPPORTED),
+            (lib.fa_paged_fwd_packed, fa._FWD, fwd, 10, 64, WORKSPACE),
+            (lib.fa_paged_fwd_packed, fa._FWD, fwd, 26, 5, INVALID), (lib.fa_paged_fwd_packed, fa._FWD, fwd, 11, 260, ALIGN)):
+        values = list(ok)
+        values[at] = bad
+        if st is fa._FWD and at == 20:
+            values[13] = values[14] = 1 << 20
+        assert fn(st.pack(st.size, *values)) == code, (fn.__name__, at, bad)
+        assert fn(st.pack(st.size + 8, *ok)) == INVALID and "bytes" in lib.fa_get_last_error().decode()
+        assert fn(None) == INVALID
+    none = list(fwd)
+    none[16] = 0  # no token
+    assert lib.fa_paged_fwd_packed(fa._FWD.pack(fa._FWD.size, *none)) == OK

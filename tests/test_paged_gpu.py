@@ -350,7 +350,7 @@ def test_empty_batch_and_refusals(cuda_lib):
                dict(k_cache=t["k_cache"][:, :, :8], v_cache=t["v_cache"][:, :, :8]),
                dict(k_cache=t["k_cache"].transpose(1, 2)), dict(kv_len=t["kv_len"].long()),
                dict(cu_q=t["cu_q"][:1]), dict(block_table=t["block_table"].float()),
-               dict(block_table=t["block_table"].cpu()), dict(scale=0.0), dict(scale=float("nan")),
+               dict(block_table=t["block_table"].cpu()), dict(scale=0.0), dict(scale=float("nan")), dict(scale=1e300), dict(max_q=1 << 40), dict(scale="x"),
                dict(out=torch.empty((3, 4, 64), dtype=torch.bfloat16, device="cuda")),
                dict(lse=torch.empty((4, 4), dtype=torch.bfloat16, device="cuda")),
                dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
