@@ -145,34 +145,54 @@ __device__ __forceinline__ long long paged_prefix(int causal, const PagedReq& r,
   return s;
 }
 
+// This thread's request of a batch that has one per thread at most: loaded, costed and placed on the
+// line once for the CTA's share and its first list.  (Later lists load again: few CTAs need one,
+// and the registers would be held through the loop.)
+struct PagedMine {
+  PagedReq r;
+  long long lin, cost;
+};
+
 // The length W of the line.  Every thread of the block (NT) calls it.
 template <int KT, int C, int NT>
-__device__ long long paged_total(const PagedParams& p, int tpt, PagedSched& s) {
-  long long mine = 0, all;
+__device__ long long paged_total(const PagedParams& p, int tpt, PagedSched& s, PagedMine& mine) {
+  long long sum = 0, all;
   for (int b = threadIdx.x; b < p.B; b += NT) {
-    const PagedReq r = paged_req(p, b);
-    mine += paged_prefix<KT, C>(p.causal, r, tpt, (r.nq + tpt - 1) / tpt);
+    mine.r = paged_req(p, b);
+    sum += paged_prefix<KT, C>(p.causal, mine.r, tpt, (mine.r.nq + tpt - 1) / tpt) * p.Hv;
   }
-  block_excl_scan<long long, NT>(mine, s.tmp, &all);
-  return all * p.Hv;
+  mine.lin = block_excl_scan<long long, NT>(sum, s.tmp, &all);
+  mine.cost = sum;
+  return all;
 }
 
 // Lists the row tiles that [lo, hi) of the line touches, PAGED_RECS at most, and sets s.stop to
 // where the listed part ends.  Every thread of the block calls it, lo < hi.
 template <int KT, int C, int NT>
-__device__ void paged_list(const PagedParams& p, int tpt, long long lo, long long hi,
-                           PagedSched& s) {
+__device__ __forceinline__ void paged_list(const PagedParams& p, int tpt, long long lo, long long hi,
+                                           const PagedMine* mine, PagedSched& s) {
+  const bool known = mine != nullptr && p.B <= NT;
   if (threadIdx.x == 0) s.stop = hi;
   long long carry = 0;
   int listed = 0;
   for (int b0 = 0; b0 < p.B && carry < hi && listed < PAGED_RECS; b0 += NT) {
     const int b = b0 + static_cast<int>(threadIdx.x);
     PagedReq r = {0, 0, 0};
-    if (b < p.B) r = paged_req(p, b);
-    const int nt = (r.nq + tpt - 1) / tpt;
-    const long long cost = paged_prefix<KT, C>(p.causal, r, tpt, nt) * p.Hv;
-    long long sum;
-    const long long lin = carry + block_excl_scan<long long, NT>(cost, s.tmp, &sum);
+    long long lin = 0, cost = 0, sum = hi;
+    int nt = 0;
+    if (known) {
+      if (b < p.B) {
+        r = mine->r;
+        cost = mine->cost;
+      }
+      lin = mine->lin;
+      nt = (r.nq + tpt - 1) / tpt;
+    } else {
+      if (b < p.B) r = paged_req(p, b);
+      nt = (r.nq + tpt - 1) / tpt;
+      cost = paged_prefix<KT, C>(p.causal, r, tpt, nt) * p.Hv;
+      lin = carry + block_excl_scan<long long, NT>(cost, s.tmp, &sum);
+    }
     // this request's first row tile that ends behind lo, where it starts, and how many from it
     // on (PAGED_RECS at most) start before hi
     int t0 = 0, count = 0;
@@ -261,8 +281,8 @@ __device__ __forceinline__ size_t paged_slot(int cta, const PagedPiece& c) {
 // Every thread of the block calls it.
 template <int KT, int C, int NT>
 __device__ __forceinline__ bool paged_share(const PagedParams& p, int tpt, PagedSched& s, long long& lo,
-                                            long long& hi) {
-  const long long W = paged_total<KT, C, NT>(p, tpt, s);
+                                            long long& hi, PagedMine& mine) {
+  const long long W = paged_total<KT, C, NT>(p, tpt, s, mine);
   const long long ctas = min(static_cast<long long>(gridDim.x), W);
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
@@ -350,6 +370,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_few_kernel(cons
   __shared__ float4 s_acc[JOIN_WARPS][32];
   __shared__ float2 s_ml[JOIN_WARPS];
   grid_dep_wait();
+  grid_dep_launch();
   const int cta = blockIdx.x;
   const int4 head = p.ws_head[cta];
   if (head.x <= 0) return;
@@ -400,6 +421,7 @@ template <typename T, int LPR>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_rows_kernel(const PagedParams p) {
   constexpr int DEPTH = 2;
   grid_dep_wait();
+  grid_dep_launch();
   const int cta = blockIdx.x;
   const int4 head = p.ws_head[cta];
   if (head.x <= 0) return;

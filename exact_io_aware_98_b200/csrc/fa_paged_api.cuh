@@ -18,6 +18,27 @@ int log2_page(int page_size) {
   return s;
 }
 
+// A launch that may overlap the kernel before it on the stream (programmatic dependent launch): every
+// kernel launched so waits for that kernel before its first access to memory.  Back to back, the
+// launch latency and the set-up of a kernel then hide behind the one before.
+template <typename... Exp, typename... Act>
+int launch_overlapped(const char* what, void (*kern)(Exp...), dim3 grid, unsigned block, size_t smem,
+                      cudaStream_t s, Act&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Act>(args)...);
+  if (e != cudaSuccess) return fail(FA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return check_launch(what);
+}
+
 // ---- rotary -----------------------------------------------------------------------------
 // Vector width for rows of d columns of which `rot` turn: 16 bytes where every row start and
 // every piece of a row allows it, else one element.
@@ -105,18 +126,8 @@ int launch_join(const fa::PagedParams& p, int ctas, bool few, cudaStream_t s) {
   const int rows = few ? fa::JOIN_WARPS / 4 : fa::JOIN_WARPS * 32 / lpr * fa::JOIN_ROWS;  // of a block
   auto* kern = few ? fa::fa_paged_join_few_kernel<T>
                    : (lpr == 16 ? fa::fa_paged_join_rows_kernel<T, 16> : fa::fa_paged_join_rows_kernel<T, 32>);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (p.rows_cap + rows - 1) / rows);
-  cfg.blockDim = dim3(fa::JOIN_WARPS * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e != cudaSuccess) return fail(FA_ERR_CUDA, "fa_paged_join_kernel: %s", cudaGetErrorString(e));
-  return check_launch("fa_paged_join_kernel");
+  return launch_overlapped("fa_paged_join_kernel", kern, dim3(ctas, (p.rows_cap + rows - 1) / rows),
+                           fa::JOIN_WARPS * 32, 0, s, p);
 }
 
 // Lays the workspace out for a variant and sets the tile fields of the parameters.
@@ -145,8 +156,8 @@ int launch_paged_simt(fa::PagedParams p, int H_kv, void* ws, cudaStream_t s) {
   auto* kern = kernels[(p.d - 1) / 32];
   int rc = set_smem(kern, static_cast<int>(smem));
   if (rc != FA_OK) return rc;
-  kern<<<v.ctas, L::THREADS, smem, s>>>(p);
-  if ((rc = check_launch("fa_paged_simt_kernel")) != FA_OK) return rc;
+  rc = launch_overlapped("fa_paged_simt_kernel", kern, dim3(v.ctas), L::THREADS, smem, s, p);
+  if (rc != FA_OK) return rc;
   return launch_join<float>(p, v.ctas, Shape::WK > 1, s);
 }
 
@@ -185,8 +196,9 @@ int launch_paged_decode(fa::PagedParams p, int H_kv, int page_size, void* ws, cu
   if ((rc = set_smem(fa::fa_paged_decode_sm100_kernel<D>, L::SMEM_ALLOC)) != FA_OK) return rc;
   {
     TimedLaunch tl("fa_paged_decode_sm100_kernel", s);
-    fa::fa_paged_decode_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mk, mv, p);
-    if ((rc = check_launch("fa_paged_decode_sm100_kernel")) != FA_OK) return rc;
+    rc = launch_overlapped("fa_paged_decode_sm100_kernel", fa::fa_paged_decode_sm100_kernel<D>, dim3(v.ctas),
+                           L::THREADS, L::SMEM_ALLOC, s, mk, mv, p);
+    if (rc != FA_OK) return rc;
   }
   return launch_join<__nv_bfloat16>(p, v.ctas, true, s);
 }
@@ -226,8 +238,9 @@ int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cud
   if ((rc = set_smem(fa::fa_paged_chunk_sm100_kernel<D>, L::SMEM_ALLOC)) != FA_OK) return rc;
   {
     TimedLaunch tl("fa_paged_chunk_sm100_kernel", s);
-    fa::fa_paged_chunk_sm100_kernel<D><<<v.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(mq, mqf, mk, mv, few, p);
-    if ((rc = check_launch("fa_paged_chunk_sm100_kernel")) != FA_OK) return rc;
+    rc = launch_overlapped("fa_paged_chunk_sm100_kernel", fa::fa_paged_chunk_sm100_kernel<D>, dim3(v.ctas),
+                           L::THREADS, L::SMEM_ALLOC, s, mq, mqf, mk, mv, few, p);
+    if (rc != FA_OK) return rc;
   }
   return launch_join<__nv_bfloat16>(p, v.ctas, false, s);
 }
@@ -305,9 +318,8 @@ int fa_rope(const void* x, void* y, const int32_t* positions, const double* inv_
                                 : (V > 1 ? rope_kernel<float, 4>(il) : rope_kernel<float, 1>(il));
   const int by = std::min(B, 65535);
   if ((B + by - 1) / by > 65535) return fail(FA_ERR_UNSUPPORTED, "B too large");
-  kern<<<dim3(static_cast<unsigned>(gx), by, (B + by - 1) / by), fa::ROPE_THREADS, 0,
-         static_cast<cudaStream_t>(stream)>>>(p);
-  return check_launch("fa_rope_kernel");
+  return launch_overlapped("fa_rope_kernel", kern, dim3(static_cast<unsigned>(gx), by, (B + by - 1) / by),
+                           fa::ROPE_THREADS, 0, static_cast<cudaStream_t>(stream), p);
 }
 
 int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t* free_pages,
@@ -348,8 +360,8 @@ int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t*
   p.max_tokens = max_tokens;
   p.page_shift = shift;
   const unsigned grid = static_cast<unsigned>((static_cast<long long>(max_tokens) + fa::PLAN_THREADS - 1) / fa::PLAN_THREADS);
-  fa::fa_paged_plan_kernel<<<grid, fa::PLAN_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return check_launch("fa_paged_plan_kernel");
+  return launch_overlapped("fa_paged_plan_kernel", fa::fa_paged_plan_kernel, dim3(grid), fa::PLAN_THREADS, 0,
+                           static_cast<cudaStream_t>(stream), p);
 }
 
 int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
@@ -437,8 +449,8 @@ int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, vo
   const bool il = (options & FA_ROPE_INTERLEAVED) != 0;
   auto* kern = dtype == FA_BF16 ? (V > 1 ? append_kernel<__nv_bfloat16, 8>(il) : append_kernel<__nv_bfloat16, 1>(il))
                                 : (V > 1 ? append_kernel<float, 4>(il) : append_kernel<float, 1>(il));
-  kern<<<static_cast<unsigned>(gx), fa::ROPE_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return check_launch("fa_paged_append_kernel");
+  return launch_overlapped("fa_paged_append_kernel", kern, dim3(static_cast<unsigned>(gx)), fa::ROPE_THREADS, 0,
+                           static_cast<cudaStream_t>(stream), p);
 }
 
 size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d) {

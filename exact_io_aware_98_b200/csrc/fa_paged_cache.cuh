@@ -68,6 +68,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) fa_paged_plan_kernel(const PlanP
   const int t_end = min(t0 + PLAN_THREADS, p.max_tokens);
   const int page = 1 << p.page_shift;
   const bool lead = blockIdx.x == 0;
+  grid_dep_wait();  // launched to overlap the kernel before, as the next one may overlap this
+  grid_dep_launch();
   const long long cursor = p.cursor == nullptr ? 0 : max(0, *p.cursor);
   long long asked = 0, pages = 0;  // sums over the requests before this round's
   for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {

@@ -140,10 +140,12 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpt = L::R / p.G;  // tokens per tile; G <= 256
 
+  grid_dep_wait();  // launched to overlap the kernel before
   grid_dep_launch();
   const int cta = blockIdx.x;
   long long x, hi;
-  if (!paged_share<BN, C, 320>(p, tpt, sched, x, hi)) return;
+  PagedMine mine = {};
+  if (!paged_share<BN, C, 320>(p, tpt, sched, x, hi, mine)) return;
   if (threadIdx.x == 0) {
     mbar_init(bar_qf, 1);
     mbar_init(bar_qe, 1);
@@ -181,7 +183,8 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
   int prev_flags = 0, prev_vs = 0, prev_it = 0, prev_acc = 0;
 
   while (x < hi) {
-    paged_list<BN, C, 320>(p, tpt, x, hi, sched);
+    // (not the first list from `mine`: the loop then keeps more registers, 2.5 % at d = 128)
+    paged_list<BN, C, 320>(p, tpt, x, hi, nullptr, sched);
     const long long stop = sched.stop;
     PagedPieces<C> pieces;
     pieces.start(p, sched, x);

@@ -121,7 +121,6 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tpt = L::R / p.G;  // G <= R
 
-  grid_dep_launch();
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&bar_full[s], 1);
@@ -130,14 +129,17 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
     *abort_flag = 0;
     fence_mbar_init();
   }
+  grid_dep_wait();  // launched to overlap the kernel before
+  grid_dep_launch();
   const int cta = blockIdx.x;
   long long x, hi;
-  if (!paged_share<KT, C, L::THREADS>(p, tpt, sched, x, hi)) return;  // else: a barrier has passed
+  PagedMine mine = {};
+  if (!paged_share<KT, C, L::THREADS>(p, tpt, sched, x, hi, mine)) return;  // else: a barrier has passed
   int it = 0;      // tiles issued (producer) or passed (consumers) so far
   bool ok = true;
 
-  while (x < hi) {
-    paged_list<KT, C, L::THREADS>(p, tpt, x, hi, sched);
+  paged_list<KT, C, L::THREADS>(p, tpt, x, hi, &mine, sched);
+  while (true) {
     const long long stop = sched.stop;
     if (warp == L::WARPS) {
       // ---------------------------------------------------------------- producer
@@ -404,7 +406,9 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
     }
     x = stop;
+    if (x >= hi) break;
     __syncthreads();  // the list is rewritten
+    paged_list<KT, C, L::THREADS>(p, tpt, x, hi, nullptr, sched);
   }
   if (warp == L::WARPS) {
     // no copy may be in flight when the CTA ends (immediate unless a wait gave up)

@@ -72,19 +72,21 @@ fa_paged_simt_kernel(const PagedParams p) {
   const int wr = warp / WK, wk = warp % WK;
   const int tpt = R / p.G;  // G <= R
 
-  grid_dep_launch();
   // zero the columns that pad d up to a multiple of 4 (read by the 16-byte accesses)
   for (int e = tid; e < (R + 2 * KT) * pitch; e += NT) s_q[e] = 0.f;
+  grid_dep_wait();  // launched to overlap the kernel before
+  grid_dep_launch();
   const int cta = blockIdx.x;
   long long x, hi;
-  if (!paged_share<KT, C, NT>(p, tpt, sched, x, hi)) return;
+  PagedMine mine = {};
+  if (!paged_share<KT, C, NT>(p, tpt, sched, x, hi, mine)) return;
   float* my_p = s_p + warp * L::P;
   // this thread's first 16-byte chunk (or element) of a tile, and the step to its next
   const int per_row = p.vec ? dv : d;
   const int ld_r = tid / per_row, ld_c = tid % per_row, ld_dr = NT / per_row, ld_dc = NT % per_row;
 
-  while (x < hi) {
-    paged_list<KT, C, NT>(p, tpt, x, hi, sched);
+  paged_list<KT, C, NT>(p, tpt, x, hi, &mine, sched);
+  while (true) {
     PagedPieces<C> pieces;
     pieces.start(p, sched, x);
     PagedPiece pc;
@@ -303,7 +305,9 @@ fa_paged_simt_kernel(const PagedParams p) {
       if (tid == 0 && pc.a == 0 && pc.b < rc.n) paged_header<C>(p, sched, rc, pc.h, cta);
     }
     x = sched.stop;
+    if (x >= hi) break;
     __syncthreads();  // the list is rewritten
+    paged_list<KT, C, NT>(p, tpt, x, hi, nullptr, sched);
   }
 }
 

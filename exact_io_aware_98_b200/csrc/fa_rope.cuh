@@ -167,6 +167,8 @@ __device__ __forceinline__ void rope_block(const RopeShape& sh, int N, int n_hea
                                            Rows& rows) {
   __shared__ float2 table[ROPE_TABLE];
   using Vec = RopeVec<T, V>;
+  grid_dep_wait();  // launched to overlap the kernel before, as the next one may overlap this
+  grid_dep_launch();
   const int half = rot / 2;
   int blk = blockIdx.x;
   const int ub = blk % sh.u_blocks;
