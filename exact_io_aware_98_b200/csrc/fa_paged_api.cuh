@@ -245,6 +245,25 @@ int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cud
   return launch_join<__nv_bfloat16>(p, v.ctas, false, s);
 }
 
+// Rows of a K/V head (tokens x heads of its group) up to which the kernels of few rows per tile run;
+// keys: K/V heads x positions that the batch's block table has room for.
+//   bf16: 16 rows, one tile.  More rows read the cache once per tile: 16 requests of 8192 keys, 32
+//   heads over 8, d 128, take 93 us with 16 rows (chunk kernel 117), 172 with 24 (116).  Where
+//   the whole cache is eight 64-key tiles per SM or less, a call is latency and not bytes, and
+//   the few-row kernel has less of it: 2 requests of 2048 keys, 48 rows: 20 us against 23.
+//   fp32: 24 rows, three tiles of 8: 4 requests of 4096 keys, 8 heads over 4, d 128: 35 us with 8
+//   rows (chunk kernel 66), 60 with 16 (69), 79 with 24 (74), 104 with 32 (77).
+long long few_rows(int dtype, long long keys) {
+  if (dtype == FA_F32) return 24;
+  return keys <= 8ll * 64 * kSms ? 48 : 16;
+}
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + bn && y < x + an;
+}
+
 // Copies a packed call's arguments (which need not be aligned) after checking their size.
 template <typename Args>
 int unpack(const Args* packed, Args* a) {
@@ -342,6 +361,20 @@ int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t*
       !aligned_to(kv_len, 4) || !aligned_to(positions, 4) || !aligned_to(slots, 8) ||
       !aligned_to(counts, 4))
     return fail(FA_ERR_ALIGN, "a pointer is not aligned to its elements");
+  {
+    // blocks read the inputs while others write: an output must not be an input
+    const size_t b4 = static_cast<size_t>(B) * 4, t4 = static_cast<size_t>(max_tokens) * 4;
+    const size_t table_bytes = (static_cast<size_t>(B - 1) * (B > 1 ? table_stride : 0) + max_pages) * 4;
+    const struct {
+      const void* p;
+      size_t n;
+    } in[4] = {{ctx_len, b4}, {new_len, b4}, {free_pages, static_cast<size_t>(n_free) * 4}, {cursor, 4}},
+      out[6] = {{cu_q, b4 + 4}, {kv_len, b4}, {positions, t4}, {slots, 2 * t4}, {counts, 16}, {block_table, table_bytes}};
+    for (const auto& i : in)
+      for (const auto& o : out)
+        if (i.n > 0 && overlap(i.p, i.n, o.p, o.n))
+          return fail(FA_ERR_INVALID, "an output overlaps an input");
+  }
   fa::PlanParams p;
   p.ctx_len = ctx_len;
   p.new_len = new_len;
@@ -499,6 +532,14 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
       ((T > 1 && q_token_stride % 8 != 0) || (H > 1 && q_head_stride % 8 != 0) ||
        (num_pages > 1 && (k_page_stride % 8 != 0 || v_page_stride % 8 != 0))))
     return fail(FA_ERR_ALIGN, "bf16 strides must be multiples of 8 elements");
+  {
+    const size_t rows_out = static_cast<size_t>(T) * H;
+    const size_t q_bytes =
+        (static_cast<size_t>(T - 1) * (T > 1 ? q_token_stride : 0) + static_cast<size_t>(H - 1) * (H > 1 ? q_head_stride : 0) + d) * es;
+    if (overlap(o, rows_out * d * es, q, q_bytes) || overlap(lse, rows_out * 4, q, q_bytes) ||
+        overlap(o, rows_out * d * es, lse, rows_out * 4))
+      return fail(FA_ERR_INVALID, "o, lse and q overlap");
+  }
   const size_t need = paged_ws_bytes(T, H / H_kv, d);
   if (workspace == nullptr || workspace_bytes < need)
     return fail(FA_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, workspace_bytes);
@@ -532,15 +573,16 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // new tokens per request: the caller's bound, or the batch's mean
   const long long rows = static_cast<long long>(max_q > 0 ? std::min(max_q, T) : (T + B - 1) / B) * p.group;
+  const bool few = rows <= few_rows(dtype, static_cast<long long>(B) * H_kv * (max_pages << shift));
   if (dtype == FA_BF16) {
-    if (rows <= 16)
+    if (few)
       return d == 64 ? launch_paged_decode<64>(p, H_kv, page_size, workspace, s)
                      : launch_paged_decode<128>(p, H_kv, page_size, workspace, s);
     return d == 64 ? launch_paged_chunk<64>(p, H_kv, page_size, workspace, s)
                    : launch_paged_chunk<128>(p, H_kv, page_size, workspace, s);
   }
-  return rows <= 8 ? launch_paged_simt<fa::PagedSimtFew>(p, H_kv, workspace, s)
-                   : launch_paged_simt<fa::PagedSimtChunk>(p, H_kv, workspace, s);
+  return few ? launch_paged_simt<fa::PagedSimtFew>(p, H_kv, workspace, s)
+             : launch_paged_simt<fa::PagedSimtChunk>(p, H_kv, workspace, s);
 }
 
 int fa_rope_packed(const fa_rope_args* args) {

@@ -225,6 +225,7 @@ int fa_rope(const void* x, void* y, const int32_t* positions, const double* inv_
  *                     in this step are written (ceil(ctx / page_size) on), the others are read.
  *   cu_q [B+1], kv_len [B], positions [max_tokens], slots [max_tokens] (int64), counts [4]:
  *       counts = {new tokens asked for, pages taken, pages short, cursor after}.
+ *   No output may overlap an input (cursor = counts + 3, say: FA_ERR_INVALID); copy between steps.
  *   Tokens beyond max_tokens are left out of the step (of cu_q and kv_len as well).  A token whose
  *   page is missing (none left, or beyond max_pages, or a negative id) gets slot -1; an entry for
  *   which no page was left becomes -1.  Padding gets position 0, slot -1.
@@ -244,6 +245,7 @@ int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t*
  *   slots      a token with a slot outside [0, num_pages * page_size) is not stored.  The slots
  *              stored to must differ; for a slot named twice it is not defined which values land.
  *   options    FA_ROPE_INTERLEAVED or 0.  d <= 1024; any alignment (element path as in fa_rope).
+ *   Other overlaps between the tensors than q_out = q are undefined.  T = 0 does nothing.
  */
 int fa_paged_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache,
                     void* v_cache, const int64_t* slots, const int32_t* positions,
@@ -259,7 +261,8 @@ size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d);
  * fa_paged_fwd -- attention of each request's new tokens over its paged cache, grouped heads as
  * in fa_fwd_gqa: O = softmax(scale Q K^T, masked) V and lse, decoding steps and prompt chunks in
  * any mix.
- *   q [T][H][d] (token and head strides in elements), o [T][H][d] and lse [T][H] contiguous.
+ *   q [T][H][d] (positive token and head strides in elements), o [T][H][d] and lse [T][H]
+ *   contiguous; the three may not overlap, and neither may the workspace overlap anything.
  *   Masks      token i of a request with nq new tokens sees the keys j < kv_len[b] with, causal
  *              != 0, j <= kv_len[b] - nq + i.  A key whose block-table entry is outside
  *              [0, num_pages) is masked.  A row with no key gets O = 0, lse = -inf.  What stale
@@ -400,7 +403,8 @@ int fa_diag_wait_timeout(int site, void* stream);
  *                            counted).
  *   fa_kernel_timing      -- enable != 0: from now on every launch of a tensor-core kernel
  *                            (fa_fwd_sm100_kernel, fa_bwd_sm100_kernel, fa_bwd_dkdv_sm100_kernel,
- *                            fa_bwd_dkdv_pair_sm100_kernel, fa_bwd_dq_sm100_kernel) is
+ *                            fa_bwd_dkdv_pair_sm100_kernel, fa_bwd_dq_sm100_kernel,
+ *                            fa_paged_decode_sm100_kernel, fa_paged_chunk_sm100_kernel) is
  *                            bracketed by two CUDA events recorded on
  *                            the launch's stream; enable == 0 stops recording.  Off by default.
  *   fa_kernel_timing_read -- waits for the recorded launches of every kernel whose name contains

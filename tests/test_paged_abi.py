@@ -36,8 +36,9 @@ def test_rope_codes(lib):
     assert _rope(lib, N=0) == OK and _rope(lib, B=0) == OK
 
 
-def _plan(lib, ctx=A, free=A, nf=4, cur=None, tab=A, ts=8, B=2, mp=8, page=16, cap=4, slots=A):
-    return lib.fa_paged_plan(ctx, A, free, nf, cur, tab, ts, B, mp, page, cap, A, A, A, slots, A, None)
+def _plan(lib, ctx=A, new=A + 256, free=A + 512, nf=4, cur=None, tab=A + 1024, ts=8, B=2, mp=8, page=16, cap=4,
+          cu=A + 2048, kv=A + 2304, pos=A + 2560, slots=A + 4096, counts=A + 8192):
+    return lib.fa_paged_plan(ctx, new, free, nf, cur, tab, ts, B, mp, page, cap, cu, kv, pos, slots, counts, None)
 
 
 def test_plan_codes(lib):
@@ -45,6 +46,10 @@ def test_plan_codes(lib):
                dict(page=8), dict(page=24), dict(page=2048), dict(cap=0), dict(slots=None)):
         assert _plan(lib, **kw) == INVALID, kw
     assert _plan(lib, slots=A + 4) == ALIGN and _plan(lib, cur=A + 1) == ALIGN
+    for kw in (dict(cur=A + 8192 + 12), dict(ctx=A + 2304), dict(new=A + 2304 + 4), dict(free=A + 1024 + 28),
+               dict(pos=A + 508), dict(counts=A + 4)):
+        assert _plan(lib, **kw) == INVALID, kw
+        assert "overlaps" in lib.fa_get_last_error().decode()
 
 
 def _append(lib, q=A, k=A, qo=A + 4096, kc=A, slots=A, pos=A, f=A, T=2, H=2, H_kv=1, d=64, rot=64,
@@ -64,7 +69,7 @@ def test_append_codes(lib):
     assert _append(lib, T=0) == OK
 
 
-def _fwd(lib, q=A, kc=A, tab=A, o=A, lse=A, T=4, B=2, H=4, H_kv=2, d=64, qt=256, qh=64, kp=2048, vp=2048, ts=8,
+def _fwd(lib, q=A, kc=A, tab=A, o=A + 65536, lse=A + 131072, T=4, B=2, H=4, H_kv=2, d=64, qt=256, qh=64, kp=2048, vp=2048, ts=8,
          page=16, pages=4, mp=8, scale=0.125, dtype=0, ws=A, wsb=1 << 30):
     return lib.fa_paged_fwd(q, kc, A, tab, A, A, o, lse, T, B, H, H_kv, d, qt, qh, kp, vp, ts, page, pages, mp, 1, scale, 1,
                             dtype, ws, wsb, None)
@@ -78,7 +83,10 @@ def test_fwd_codes(lib):
     for kw in (dict(d=96, kp=1 << 20, vp=1 << 20), dict(d=256, dtype=1, kp=1 << 20, vp=1 << 20), dict(T=1 << 25),
                dict(mp=1 << 28, ts=1 << 28)):
         assert _fwd(lib, **kw) == UNSUPPORTED, kw
-    for kw in (dict(q=A + 8), dict(kc=A + 8), dict(o=A + 4), dict(lse=A + 4), dict(tab=A + 2), dict(qt=260),
+    for kw in (dict(o=A), dict(o=A + 2032), dict(lse=A + 16), dict(o=A + 131072)):
+        assert _fwd(lib, **kw) == INVALID, kw
+        assert "overlap" in lib.fa_get_last_error().decode()
+    for kw in (dict(q=A + 8), dict(kc=A + 8), dict(o=A + 65540), dict(lse=A + 131076), dict(tab=A + 2), dict(qt=260),
                dict(qh=4), dict(kp=2052)):
         assert _fwd(lib, **kw) == ALIGN, kw
     for kw in (dict(ws=None), dict(wsb=64), dict(ws=A + 16)):
@@ -129,10 +137,11 @@ def test_packed_calls(lib):
     """The packed forms refuse what their calls refuse, and a structure of another size."""
     A64 = A
     rope = [A64, A64 + 4096, 0, A64, 0, 512, 256, 64, 512, 256, 64, 0, 1, 2, 4, 64, 64, 0, 0, 1.0]
-    plan = [A64, A64, A64, 0, A64, A64, A64, A64, A64, A64, 0, 8, 4, 2, 8, 16, 4, 0]
+    plan = [A64, A64 + 256, A64 + 512, 0, A64 + 1024, A64 + 2048, A64 + 2304, A64 + 2560, A64 + 8192, A64 + 4096, 0, 8, 4,
+            2, 8, 16, 4, 0]
     append = [A64, A64, A64, A64 + 4096, A64, A64, A64, A64, A64, 0, 128, 64, 64, 64, 64, 64, 128, 64, 1024, 1024,
               2, 2, 1, 64, 64, 16, 4, 0, 0, 1.0]
-    fwd = [A64, A64, A64, A64, A64, A64, A64, A64, A64, 0, 1 << 30, 256, 64, 2048, 2048, 8, 4, 2, 4, 2, 64, 16, 4, 8, 1,
+    fwd = [A64, A64, A64, A64, A64, A64, A64 + 65536, A64 + 131072, A64, 0, 1 << 30, 256, 64, 2048, 2048, 8, 4, 2, 4, 2, 64, 16, 4, 8, 1,
            1, 0, 0.125]
     for fn, st, ok, at, bad, code in (
             (lib.fa_rope_packed, fa._ROPE, rope, 16, 63, INVALID), (lib.fa_rope_packed, fa._ROPE, rope, 0, A + 1, ALIGN),

@@ -202,6 +202,11 @@ CASES = [
     ([(257, 513)], 2, 2, 64, 16, "bf16", True, 257),
     ([(1, 300)] * 300, 2, 1, 64, 16, "bf16", True, 1),  # many small requests
     ([(0, 5)] * 40 + [(2, 3)] * 600, 1, 1, 64, 16, "bf16", True, 2),
+    ([(1, 3)] * 9000, 1, 1, 64, 16, "bf16", True, 1),   # more row tiles than a CTA lists at a time
+    ([(1, 3), (2, 2), (0, 7)] * 3000, 2, 2, 64, 16, "bf16", True, 99),
+    ([(40, 900)] * 3, 8, 2, 128, 64, "bf16", True, 40),
+    ([(12, 900), (3, 40)], 8, 2, 64, 64, "bf16", True, 12),  # 48 rows over a small cache
+    ([(1, 2)] * 9000, 1, 1, 8, 16, "f32", True, 1),
     (DECODE, 6, 2, 80, 16, "f32", True, 1),
     (RAGGED, 4, 2, 80, 16, "f32", True, 200),
     (RAGGED, 3, 1, 33, 32, "f32", False, 200),       # odd head dimension
@@ -333,6 +338,134 @@ def test_two_streams_at_once(cuda_lib):
         n = sum(q for q, _ in cases[i]["lens"])
         for o, lse in got[i]:
             assert torch.equal(o[:n], want[i][0][:n]) and torch.equal(lse[:n], want[i][1][:n])
+
+
+@pytest.mark.parametrize("dtype,d,max_q", [("bf16", 64, 1), ("bf16", 64, 500), ("bf16", 128, 1), ("bf16", 128, 500),
+                                           ("f32", 20, 1), ("f32", 20, 500)])
+def test_offsets_beyond_32_bits(cuda_lib, dtype, d, max_q):
+    """The pages of a cache of more than 2^31 elements, at its far end: append, then attention.  All
+    other rows of the cache hold whatever the allocation held."""
+    fa = cuda_lib
+    page, H, H_kv = 16, 2, 1
+    n_pages = (1 << 31) // (H_kv * page * d) + 40
+    g = torch.Generator().manual_seed(d)
+    dt = TORCH[dtype]
+    kc = torch.empty((n_pages, H_kv, page, d), dtype=dt, device="cuda")
+    vc = torch.empty_like(kc)
+    lens = [(2, 50), (30, 77)]
+    c = paged_case(lens, H, H_kv, d, page, dtype, seed=d)
+    table = torch.tensor([[n_pages - 1 - i for i in range(10)], [n_pages - 20 - i for i in range(10)]],
+                         dtype=torch.int32, device="cuda")
+    for b, (_, nk) in enumerate(lens):
+        k, v = (torch.from_numpy(x).to(dt).transpose(0, 1).contiguous().cuda() for x in c["dense"][b])
+        pos = torch.arange(nk, device="cuda")
+        slots = table[b].long()[pos // page] * page + pos % page
+        assert int(slots.min()) * H_kv * d > (1 << 31) - 40 * page * d
+        fa.paged_append(k, v, kc, vc, slots)
+    q = c["q"].cuda()
+    o, lse = fa.paged_fwd(q, kc, vc, table, c["kv_len"].cuda(), c["cu_q"].cuda(), scale=syn.scale_for(d), max_q=max_q)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 0
+    check_paged(c, o, lse, True, syn.scale_for(d))
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 7), ("f32", 64)])
+@pytest.mark.parametrize("max_q", [1, 500])
+def test_outputs_at_any_allowed_alignment(cuda_lib, dtype, d, max_q):
+    """o, lse, q and the caches 16-byte aligned and no more."""
+    fa = cuda_lib
+    c = paged_case([(3, 70), (20, 40), (1, 300)], 4, 2, d, 16, dtype, seed=8)
+    t = to_cuda(c)
+    es = 2 if dtype == "bf16" else 4
+
+    def shifted(x, step):
+        flat = torch.empty(x.numel() + step, dtype=x.dtype, device="cuda")
+        y = flat[step:].view(x.shape)
+        y.copy_(x)
+        assert y.data_ptr() % 32 == 16
+        return y
+    q, k, v = (shifted(t[n].contiguous(), 16 // es) for n in ("q", "k_cache", "v_cache"))
+    o = shifted(torch.full(c["q"].shape, 2.0, dtype=TORCH[dtype]), 16 // es)
+    lse = shifted(torch.full(c["q"].shape[:2], 2.0), 4)
+    o0, l0 = o.clone(), lse.clone()
+    fa.paged_fwd(q, k, v, t["block_table"], t["kv_len"], t["cu_q"], scale=syn.scale_for(d), max_q=max_q, out=o, lse=lse)
+    check_paged(c, o, lse, True, syn.scale_for(d), o_before=o0, lse_before=l0)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 33)])
+@pytest.mark.parametrize("max_q", [1, 500])
+def test_a_bad_request_stays_alone(cuda_lib, dtype, d, max_q):
+    """NaN and infinities in one request's keys, values and queries change no other request."""
+    fa = cuda_lib
+    c = paged_case([(1, 200), (5, 90), (1, 40), (9, 300)], 4, 2, d, 16, dtype, seed=12, stale=False)
+    t = to_cuda(c)
+    args = lambda: (t["q"], t["k_cache"], t["v_cache"], t["block_table"], t["kv_len"], t["cu_q"])
+    want, wl = fa.paged_fwd(*args(), max_q=max_q)
+    bad = t["block_table"][1][:6].long()
+    t["k_cache"][bad[1]] = float("nan")
+    t["k_cache"][bad[3]] = float("inf")
+    t["v_cache"][bad[2]] = float("nan")
+    t["q"][1:6, 0] = float("nan")
+    got, gl = fa.paged_fwd(*args(), max_q=max_q)
+    for rows in (slice(0, 1), slice(6, 16)):
+        assert torch.equal(got[rows], want[rows]) and torch.equal(gl[rows], wl[rows])
+    assert torch.isnan(got[1:6]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_captured_step_serves(cuda_lib, dtype):
+    """Plan, append and attention captured as one graph of fixed capacity, replayed while lengths,
+    tokens, cursor and tables live on the device, against the same calls one by one."""
+    fa = cuda_lib
+    H, H_kv, d, page, cap = 4, 2, 64, 16, 48
+    dt = TORCH[dtype]
+    g = torch.Generator().manual_seed(3)
+    fi, m = fa.rope_frequencies(d)
+    steps = [[40, 0, 3], [1, 1, 1], [1, 30, 1], [0, 1, 17], [1, 1, 1]]
+    xs = [torch.randn((cap, (H + 2 * H_kv) * d), generator=g).to(dt).cuda() for _ in steps]
+    free = torch.randperm(40, generator=g).to(torch.int32).cuda()
+
+    def fresh():
+        s = dict(kc=torch.zeros((40, H_kv, page, d), dtype=dt, device="cuda"), ctx=torch.zeros(3, dtype=torch.int32, device="cuda"),
+                 new=torch.zeros(3, dtype=torch.int32, device="cuda"), cursor=torch.zeros(1, dtype=torch.int32, device="cuda"),
+                 table=torch.full((3, 8), -1, dtype=torch.int32, device="cuda"), x=torch.zeros_like(xs[0]),
+                 plan=fa.PagedPlan.empty(3, cap), o=torch.zeros((cap, H, d), dtype=dt, device="cuda"),
+                 lse=torch.zeros((cap, H), device="cuda"), q=torch.empty((cap, H, d), dtype=dt, device="cuda"),
+                 ws=torch.empty(fa.paged_workspace_size(cap, 3, H, H_kv, d), dtype=torch.uint8, device="cuda"))
+        s["vc"] = torch.zeros_like(s["kc"])
+        return s
+
+    def step(s):
+        p = fa.paged_plan(s["ctx"], s["new"], free, s["table"], page, cap, cursor=s["cursor"], out=s["plan"])
+        q, k, v = (t.view(cap, -1, d) for t in s["x"].split([H * d, H_kv * d, H_kv * d], 1))
+        fa.paged_append(k, v, s["kc"], s["vc"], p.slots, positions=p.positions, inv_freq=fi, q=q, q_out=s["q"])
+        fa.paged_fwd(s["q"], s["kc"], s["vc"], s["table"], p.kv_len, p.cu_q, max_q=cap, out=s["o"], lse=s["lse"],
+                     workspace=s["ws"])
+        s["ctx"].copy_(p.kv_len)
+        s["cursor"].copy_(p.counts[3:4])
+
+    a, b = fresh(), fresh()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # every kernel once before the capture, and not on the default stream
+        step(b)
+        b["ctx"].zero_()
+        b["cursor"].zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(b)
+    for n, x in zip(steps, xs):
+        for s in (a, b):
+            s["new"].copy_(torch.tensor(n, dtype=torch.int32))
+            s["x"].copy_(x)
+            s["o"].zero_()
+            s["lse"].zero_()
+        step(a)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in ("o", "lse", "kc", "vc", "table", "ctx", "cursor"):
+            assert torch.equal(a[k], b[k]), k
+    assert a["ctx"].cpu().tolist() == [43, 33, 23] and fa.device_status() == 0
 
 
 def test_empty_batch_and_refusals(cuda_lib):
