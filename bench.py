@@ -106,9 +106,13 @@ def select_peak(peaks: dict, clocks: dict) -> tuple[float, str]:
 
 
 def csrc_hash() -> str:
+    """Hash of the sources that the kernels of the traffic table are built from (the rotary and
+    paged-cache files are not among them: fa_lib.cu includes them behind fa_api.cu)."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "exact_io_aware_98_b200", "csrc")
     for name in sorted(os.listdir(d)):
+        if name.startswith(("fa_paged", "fa_rope", "fa_lib")):
+            continue
         with open(os.path.join(d, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]

@@ -10,7 +10,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfa.so")
-MAIN = os.path.join(CSRC, "fa_api.cu")
+MAIN = os.path.join(CSRC, "fa_lib.cu")
 
 
 def _sources():

@@ -8,7 +8,6 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <utility>
@@ -20,12 +19,6 @@
 #include "fa_bwd_dq_sm100.cuh"
 #include "fa_bwd_sm100.cuh"
 #include "fa_fwd_sm100.cuh"
-#include "fa_paged.cuh"
-#include "fa_paged_cache.cuh"
-#include "fa_paged_chunk_sm100.cuh"
-#include "fa_paged_decode_sm100.cuh"
-#include "fa_paged_simt.cuh"
-#include "fa_rope.cuh"
 #include "fa_simt.cuh"
 #include "ptx.cuh"
 
@@ -890,7 +883,3 @@ extern "C" int fa_bwd_noalloc(const void* q, const void* k, const void* v, const
   return bwd_impl(q, k, v, o, lse, dO, dq, dk, dv, B, H, H, N, d, scale, causal, block_mask,
                   kv_len, dtype, scratch, kNoAllocScratchBytes, stream, false);
 }
-
-// ---------------------------------------------------------------------------------------------
-// Rotary positions and the paged cache.
-#include "fa_paged_api.cuh"

@@ -1,6 +1,6 @@
 // fa_paged_api.cuh -- host side of the rotary and paged-cache entry points: argument checks,
-// the choice of kernel and launch shape, launches.  Included by fa_api.cu, whose helpers
-// (fail, check_launch, launch_ex, set_smem, tensor-map encoding) it uses.
+// the choice of kernel and launch shape, launches.  Included by fa_lib.cu behind fa_api.cu,
+// whose helpers (fail, check_launch, set_smem, TimedLaunch, encode_fn) it uses.
 #pragma once
 
 namespace {
