@@ -101,9 +101,8 @@ size_t paged_ws_part(long long T, int group, int d, PagedShape v, int* rows_cap,
 
 // CTAs of a CUDA-core variant: what shared memory lets an SM hold, up to what its registers are
 // kept for.
-template <typename Shape>
-PagedShape simt_shape(int d) {
-  using L = fa::PagedSimtLayout<Shape>;
+template <typename L>
+PagedShape f32_shape(int d) {
   const int per_sm = static_cast<int>(std::min<size_t>(L::ctas((d + 31) / 32), 233472 / (L::bytes(d) + 1024)));
   return {L::R, kSms * per_sm};
 }
@@ -113,7 +112,7 @@ PagedShape chunk_shape(int d) { return {256, kSms * (d == 64 ? fa::PagedChunkLay
 
 size_t paged_ws_bytes(long long T, int group, int d) {
   size_t n = 0;
-  for (const PagedShape v : {simt_shape<fa::PagedSimtFew>(d), simt_shape<fa::PagedSimtChunk>(d), decode_shape(),
+  for (const PagedShape v : {f32_shape<fa::PagedF32Few>(d), f32_shape<fa::PagedF32Chunk>(d), decode_shape(),
                              chunk_shape(d)})
     n = std::max(n, paged_ws_part(T, group, d, v, nullptr, nullptr, nullptr));
   return n;
@@ -144,21 +143,17 @@ void paged_tiles(fa::PagedParams& p, PagedShape v, int H_kv, void* ws) {
   p.ws_o = reinterpret_cast<float*>(b + off_o);
 }
 
-template <typename Shape>
-int launch_paged_simt(fa::PagedParams p, int H_kv, void* ws, cudaStream_t s) {
-  using L = fa::PagedSimtLayout<Shape>;
-  const PagedShape v = simt_shape<Shape>(p.d);
+template <typename L>
+int launch_paged_f32(void (*kern)(fa::PagedParams), fa::PagedParams p, int H_kv, bool few, void* ws,
+                     cudaStream_t s) {
+  const PagedShape v = f32_shape<L>(p.d);
   paged_tiles(p, v, H_kv, ws);
   const size_t smem = L::bytes(p.d);
-  void (*const kernels[4])(const fa::PagedParams) = {
-      fa::fa_paged_simt_kernel<Shape, 1>, fa::fa_paged_simt_kernel<Shape, 2>,
-      fa::fa_paged_simt_kernel<Shape, 3>, fa::fa_paged_simt_kernel<Shape, 4>};
-  auto* kern = kernels[(p.d - 1) / 32];
   int rc = set_smem(kern, static_cast<int>(smem));
   if (rc != FA_OK) return rc;
-  rc = launch_overlapped("fa_paged_simt_kernel", kern, dim3(v.ctas), L::THREADS, smem, s, p);
+  rc = launch_overlapped("fa_paged_f32_kernel", kern, dim3(v.ctas), L::THREADS, smem, s, p);
   if (rc != FA_OK) return rc;
-  return launch_join<float>(p, v.ctas, Shape::WK > 1, s);
+  return launch_join<float>(p, v.ctas, few, s);
 }
 
 // 4-D view [page][H_kv][page_size][d] bf16 of a cache, 128-byte swizzled boxes of 64 columns and
@@ -252,7 +247,7 @@ int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cud
 //   the whole cache is eight 64-key tiles per SM or less, a call is latency and not bytes, and
 //   the few-row kernel has less of it: 2 requests of 2048 keys, 48 rows: 20 us against 23.
 //   fp32: 24 rows, three tiles of 8: 4 requests of 4096 keys, 8 heads over 4, d 128: 35 us with 8
-//   rows (chunk kernel 66), 60 with 16 (69), 79 with 24 (74), 104 with 32 (77).
+//   rows (chunk kernel 85), 59 with 16 (87), 78 with 24 (89), 101 with 32 (91).
 long long few_rows(int dtype, long long keys) {
   if (dtype == FA_F32) return 24;
   return keys <= 8ll * 64 * kSms ? 48 : 16;
@@ -581,8 +576,16 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
     return d == 64 ? launch_paged_chunk<64>(p, H_kv, page_size, workspace, s)
                    : launch_paged_chunk<128>(p, H_kv, page_size, workspace, s);
   }
-  return few ? launch_paged_simt<fa::PagedSimtFew>(p, H_kv, workspace, s)
-             : launch_paged_simt<fa::PagedSimtChunk>(p, H_kv, workspace, s);
+  using Kernel = void (*)(fa::PagedParams);
+  const int nc = (d - 1) / 32;
+  if (few) {
+    const Kernel kernels[4] = {fa::fa_paged_f32_few_kernel<1>, fa::fa_paged_f32_few_kernel<2>,
+                               fa::fa_paged_f32_few_kernel<3>, fa::fa_paged_f32_few_kernel<4>};
+    return launch_paged_f32<fa::PagedF32Few>(kernels[nc], p, H_kv, true, workspace, s);
+  }
+  const Kernel kernels[4] = {fa::fa_paged_f32_chunk_kernel<1>, fa::fa_paged_f32_chunk_kernel<2>,
+                             fa::fa_paged_f32_chunk_kernel<3>, fa::fa_paged_f32_chunk_kernel<4>};
+  return launch_paged_f32<fa::PagedF32Chunk>(kernels[nc], p, H_kv, false, workspace, s);
 }
 
 int fa_rope_packed(const fa_rope_args* args) {
