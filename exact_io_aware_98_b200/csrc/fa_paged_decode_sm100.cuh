@@ -12,7 +12,7 @@
 // per cycle, a 64-key tile (d = 128) takes 1490 cycles to arrive, and a group needs about 500
 // for it, so the stream, not the arithmetic, sets the pace.
 //
-// Page ids are fetched one tile ahead.  A page that the table does not name, or that lies behind
+// Page ids are fetched 8 to 32 tiles ahead.  A page that the table does not name, or that lies behind
 // the last key, is read as an out-of-range page, which TMA fills with zeros without reading.
 // Rows of the last page behind the last key may hold anything: their scores are replaced and
 // their V elements cleared in registers.
@@ -84,26 +84,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Walks over the key tiles of the listed pieces in order.
-template <int C>
-struct PagedTileWalk {
-  PagedPieces<C> pieces;
-  PagedPiece pc;
-  int t;
-  __device__ __forceinline__ bool start(const PagedParams& p, const PagedSched& s, long long x0) {
-    pieces.start(p, s, x0);
-    const bool any = pieces.next(p, s, pc);
-    t = pc.a;
-    return any;
-  }
-  __device__ __forceinline__ bool next(const PagedParams& p, const PagedSched& s) {
-    if (++t < pc.b) return true;
-    if (!pieces.next(p, s, pc)) return false;
-    t = pc.a;
-    return true;
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(PagedDecodeLayout<D>::THREADS, 1)
 fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -147,42 +127,57 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int np = KT / box;                     // pages in a tile
       const int part = lane / (np * L::SUB);       // 0: K, 1: V, more: idle
       const int pg = lane / L::SUB % np, sub = lane % L::SUB;
-      // this lane's page of a tile, and whether it lies behind the last key (not looked up then)
-      auto page_id = [&](const PagedTileWalk<C>& w, bool& behind) -> int {
-        const PagedRec& rc = sched.rec[w.pc.rec];
-        const int j = w.t * KT + pg * box;
-        behind = j >= paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok);
-        return behind ? -1 : p.table[rc.b * p.table_stride + (j >> p.page_shift)];
+      // The pages of 32 / np tiles from t0 on, one per lane (-1 behind the last key: not looked up).
+      // Fetched a batch ahead: a tile of 16 KB (d = 64) arrives faster than a table entry.
+      const int batch = 32 / np;
+      auto pages_of = [&](const PagedPiece& q, int t0) -> int {
+        const PagedRec& rc = sched.rec[q.rec];
+        const int j = t0 * KT + lane * box;
+        if (j >= paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok)) return -1;
+        return p.table[rc.b * p.table_stride + (j >> p.page_shift)];
       };
-      PagedTileWalk<C> w;
-      bool more = w.start(p, sched, x);
-      bool behind = false, behind_next = false;
-      int id = more ? page_id(w, behind) : 0;
+      PagedPieces<C> pieces;
+      pieces.start(p, sched, x);
+      PagedPiece pc, after;
+      bool more = pieces.next(p, sched, pc);
+      int ids = more ? pages_of(pc, pc.a) : 0;
       while (more && ok) {
-        const int h = w.pc.h / p.splits, row = (w.t * KT) & ((1 << p.page_shift) - 1);
-        more = w.next(p, sched);
-        const int id_next = more ? page_id(w, behind_next) : 0;
-        const bool there = id >= 0 && id < p.num_pages;
-        // groups of 16 keys whose page the table does not name
-        const bool bad16 = __shfl_sync(0xffffffffu, !there && !behind, (16 * (lane & 3) / box) * L::SUB);
-        const unsigned bad = __ballot_sync(0xffffffffu, lane < KT / 16 && bad16);
-        const int s = it % ST;
-        if (it >= ST)
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar_empty[s], ((it / ST) - 1) & 1, abort_flag,
-                                                 SITE_PDEC_EMPTY));
-        if (!ok) break;
-        if (lane == 0) {
-          s_bad[s] = static_cast<int>(bad);
-          mbar_arrive_expect_tx(&bar_full[s], L::STAGE);
+        const PagedRec& rc = sched.rec[pc.rec];
+        const int keys = paged_keys(p.causal, rc.kv, rc.pos0, rc.ntok), h = pc.h / p.splits;
+        more = pieces.next(p, sched, after);
+        for (int t0 = pc.a; t0 < pc.b && ok; t0 += batch) {
+          int ids_next = 0;
+          if (t0 + batch < pc.b) ids_next = pages_of(pc, t0 + batch);
+          else if (more) ids_next = pages_of(after, after.a);
+          const bool mine_bad = (ids < 0 || ids >= p.num_pages) && t0 * KT + lane * box < keys;
+          const bool any_bad = __any_sync(0xffffffffu, mine_bad);
+          for (int t = t0; t < min(pc.b, t0 + batch); ++t) {
+            const int id = __shfl_sync(0xffffffffu, ids, (t - t0) * np + pg);
+            unsigned bad = 0;  // groups of 16 keys whose page the table does not name
+            if (any_bad) {
+              const bool b16 = __shfl_sync(0xffffffffu, mine_bad, (t - t0) * np + 16 * (lane & 3) / box);
+              bad = __ballot_sync(0xffffffffu, lane < KT / 16 && b16);
+            }
+            const int s = it % ST;
+            if (it >= ST)
+              ok = __all_sync(0xffffffffu, mbar_wait(&bar_empty[s], ((it / ST) - 1) & 1, abort_flag,
+                                                     SITE_PDEC_EMPTY));
+            if (!ok) break;
+            if (lane == 0) {
+              s_bad[s] = static_cast<int>(bad);
+              mbar_arrive_expect_tx(&bar_full[s], L::STAGE);
+            }
+            __syncwarp();
+            if (part < 2)
+              tma_load_4d(smem + s * L::STAGE + part * L::TILE + sub * L::SUBTILE + pg * box * 128,
+                          part == 0 ? &tm_k : &tm_v, &bar_full[s], sub * 64,
+                          (t * KT) & ((1 << p.page_shift) - 1), h,
+                          id >= 0 && id < p.num_pages ? id : p.num_pages);
+            ++it;
+          }
+          ids = ids_next;
         }
-        __syncwarp();
-        if (part < 2)
-          tma_load_4d(smem + s * L::STAGE + part * L::TILE + sub * L::SUBTILE + pg * box * 128,
-                      part == 0 ? &tm_k : &tm_v, &bar_full[s], sub * 64, row, h,
-                      there ? id : p.num_pages);
-        ++it;
-        id = id_next;
-        behind = behind_next;
+        pc = after;
       }
     } else {
       // ---------------------------------------------------------------- consumers
