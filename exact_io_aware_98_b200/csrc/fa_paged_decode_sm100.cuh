@@ -2,7 +2,7 @@
 // rows (tokens x query heads of a group) per tile, so that each key is used a few times only and
 // the cache's bytes are what counts.
 //
-// Bound by HBM: K and V are read once.  The loop therefore is a stream: one producer warp keeps a
+// Bound by HBM: K and V are read once.  The loop therefore is a stream: two producer warps (K, V) keep a
 // ring of 64-key K/V tiles filled by TMA (one box per page and 64 columns; 128-byte swizzle),
 // and eight consumer warps, in two groups that take alternate tiles, work on 16 keys each with
 // warp-level m16n8k16 MMAs -- the 16 rows fill one such tile, where a tcgen05 tile would be 128
@@ -31,7 +31,7 @@ struct PagedDecodeLayout {
   static constexpr int R = 16, KT = 64;
   static constexpr int C = 1;                        // an item's constant, in key tiles
   static constexpr int WARPS = 8;                    // consumers
-  static constexpr int THREADS = (WARPS + 1) * 32;
+  static constexpr int THREADS = (WARPS + 2) * 32;   // and two producers: K, V
   static constexpr int SUB = D / 64;                 // 64-column (128-byte) sub-tiles
   static constexpr int SUBTILE = KT * 128;           // bytes
   static constexpr int TILE = KT * D * 2;            // one K or V tile
@@ -103,7 +103,7 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
 
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_full[s], 2);
       mbar_init(&bar_empty[s], L::WARPS / 2);
     }
     *abort_flag = 0;
@@ -121,11 +121,12 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
   paged_list<KT, C, L::THREADS>(p, tpt, x, hi, &mine, sched);
   while (true) {
     const long long stop = sched.stop;
-    if (warp == L::WARPS) {
-      // ---------------------------------------------------------------- producer
+    if (warp >= L::WARPS) {
+      // ---------------------------------------------------------------- producers (K, V)
       const int box = min(1 << p.page_shift, KT);  // rows of a page in a tile
       const int np = KT / box;                     // pages in a tile
-      const int part = lane / (np * L::SUB);       // 0: K, 1: V, more: idle
+      const int part = warp - L::WARPS;            // 0: K, 1: V
+      const bool issues = lane < np * L::SUB;
       const int pg = lane / L::SUB % np, sub = lane % L::SUB;
       // The pages of 32 / np tiles from t0 on, one per lane (-1 behind the last key: not looked up).
       // Fetched a batch ahead: a tile of 16 KB (d = 64) arrives faster than a table entry.
@@ -164,11 +165,11 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                      SITE_PDEC_EMPTY));
             if (!ok) break;
             if (lane == 0) {
-              s_bad[s] = static_cast<int>(bad);
-              mbar_arrive_expect_tx(&bar_full[s], L::STAGE);
+              if (part == 0) s_bad[s] = static_cast<int>(bad);
+              mbar_arrive_expect_tx(&bar_full[s], L::TILE);
             }
             __syncwarp();
-            if (part < 2)
+            if (issues)
               tma_load_4d(smem + s * L::STAGE + part * L::TILE + sub * L::SUBTILE + pg * box * 128,
                           part == 0 ? &tm_k : &tm_v, &bar_full[s], sub * 64,
                           (t * KT) & ((1 << p.page_shift) - 1), h,
@@ -405,7 +406,7 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
     __syncthreads();  // the list is rewritten
     paged_list<KT, C, L::THREADS>(p, tpt, x, hi, nullptr, sched);
   }
-  if (warp == L::WARPS) {
+  if (warp >= L::WARPS) {
     // no copy may be in flight when the CTA ends (immediate unless a wait gave up)
     for (int r = max(0, it - ST); r < it; ++r) mbar_wait_drain(&bar_full[r % ST], (r / ST) & 1, SITE_PDEC_DRAIN);
   }
