@@ -2,8 +2,10 @@
 // rows (tokens x query heads of a group) per tile, so that each key is used a few times only and
 // the cache's bytes are what counts.
 //
-// Bound by HBM: K and V are read once.  The loop therefore is a stream: two producer warps (K, V) keep a
-// ring of 64-key K/V tiles filled by TMA (one box per page and 64 columns; 128-byte swizzle),
+// Bound by HBM: K and V are read once.  The loop therefore is a stream: four producer warps keep a
+// ring of 64-key K/V tiles filled by TMA (one box per page and 64 columns; 128-byte swizzle; a
+// warp issues its boxes one after the other, so 16-row pages want several warps: 3.9 TB/s with
+// one, 4.6 with two, 5.0 with four at d = 64),
 // and eight consumer warps, in two groups that take alternate tiles, work on 16 keys each with
 // warp-level m16n8k16 MMAs -- the 16 rows fill one such tile, where a tcgen05 tile would be 128
 // rows of which 112 are idle, and the S and P of a warp never leave its registers.  Each warp
@@ -31,7 +33,8 @@ struct PagedDecodeLayout {
   static constexpr int R = 16, KT = 64;
   static constexpr int C = 1;                        // an item's constant, in key tiles
   static constexpr int WARPS = 8;                    // consumers
-  static constexpr int THREADS = (WARPS + 2) * 32;   // and two producers: K, V
+  static constexpr int PRODUCERS = 4;                // two for K, two for V
+  static constexpr int THREADS = (WARPS + PRODUCERS) * 32;
   static constexpr int SUB = D / 64;                 // 64-column (128-byte) sub-tiles
   static constexpr int SUBTILE = KT * 128;           // bytes
   static constexpr int TILE = KT * D * 2;            // one K or V tile
@@ -103,7 +106,7 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
 
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&bar_full[s], 2);
+      mbar_init(&bar_full[s], L::PRODUCERS);
       mbar_init(&bar_empty[s], L::WARPS / 2);
     }
     *abort_flag = 0;
@@ -122,11 +125,12 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
   while (true) {
     const long long stop = sched.stop;
     if (warp >= L::WARPS) {
-      // ---------------------------------------------------------------- producers (K, V)
+      // ---------------------------------------------------------------- producers
       const int box = min(1 << p.page_shift, KT);  // rows of a page in a tile
       const int np = KT / box;                     // pages in a tile
-      const int part = warp - L::WARPS;            // 0: K, 1: V
-      const bool issues = lane < np * L::SUB;
+      const int part = (warp - L::WARPS) & 1;      // 0: K, 1: V; two warps take its boxes by turns
+      const bool issues = lane < np * L::SUB && (lane & 1) == ((warp - L::WARPS) >> 1);
+      const int bytes = __popc(__ballot_sync(0xffffffffu, issues)) * box * 128;
       const int pg = lane / L::SUB % np, sub = lane % L::SUB;
       // The pages of 32 / np tiles from t0 on, one per lane (-1 behind the last key: not looked up).
       // Fetched a batch ahead: a tile of 16 KB (d = 64) arrives faster than a table entry.
@@ -165,8 +169,9 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
                                                      SITE_PDEC_EMPTY));
             if (!ok) break;
             if (lane == 0) {
-              if (part == 0) s_bad[s] = static_cast<int>(bad);
-              mbar_arrive_expect_tx(&bar_full[s], L::TILE);
+              if (warp == L::WARPS) s_bad[s] = static_cast<int>(bad);
+              if (bytes > 0) mbar_arrive_expect_tx(&bar_full[s], bytes);
+              else mbar_arrive(&bar_full[s]);
             }
             __syncwarp();
             if (issues)
