@@ -18,8 +18,8 @@
 // leaves the item whole.  So a batch of any mix of lengths loads all SMs alike, a single long request is
 // spread over all of them, and every CTA has at most one item that it continues for the CTA
 // before it and at most one that it leaves unfinished.  Those two pieces go to the workspace as
-// unnormalised fp32 sums with their row maximum and row sum; fa_paged_join kernels adds them in
-// the order of the keys.  Every other item is finished where it was computed.  The division
+// unnormalised fp32 sums with their row maximum and row sum; a join kernel adds them in the order of
+// the keys.  Every other item is finished where it was computed.  The division
 // depends on the lengths only, so results do not vary between runs.  Each CTA computes it from
 // the lengths on its own: no host copy of the lengths, no extra launch, and a captured call
 // follows lengths that change on the device.
@@ -50,7 +50,7 @@ struct PagedParams {
   int page_shift, num_pages, max_pages;
   int causal;
   float scale2;                // scale * log2(e)
-  // workspace: headers [ctas], row statistics [ctas][2][rows_cap], sums [ctas][2][rows_cap][pitch]
+  // workspace: headers [ctas][2], row statistics [ctas][2][rows_cap], sums [ctas][2][rows_cap][pitch]
   int4* ws_head;
   float2* ws_ml;
   float* ws_o;
@@ -277,18 +277,18 @@ __device__ __forceinline__ size_t paged_slot(int cta, const PagedPiece& c) {
   return static_cast<size_t>(cta) * 2 + (c.a > 0 ? 0 : 1);
 }
 
-// Start of a CTA: its share [lo, hi) of the line, and an empty header.  false: nothing to do.
-// Every thread of the block calls it.
-template <int KT, int C, int NT>
+// Start of a CTA: its share [lo, hi) of the line, and empty headers.  false: nothing to do.
+// Every thread of the block calls it.  LEAST: the least share that is worth a CTA, in key tiles.
+template <int KT, int C, int NT, int LEAST = 1>
 __device__ __forceinline__ bool paged_share(const PagedParams& p, int tpt, PagedSched& s, long long& lo,
                                             long long& hi, PagedMine& mine) {
   const long long W = paged_total<KT, C, NT>(p, tpt, s, mine);
-  const long long ctas = min(static_cast<long long>(gridDim.x), W);
+  const long long ctas = min(static_cast<long long>(gridDim.x), (W + LEAST - 1) / LEAST);
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     s.W = W;
     s.ctas = ctas;
-    p.ws_head[cta] = make_int4(0, 0, 0, 0);
+    p.ws_head[2 * cta] = p.ws_head[2 * cta + 1] = make_int4(0, 0, 0, 0);
   }
   if (cta >= ctas) return false;
   lo = W * cta / ctas;
@@ -296,15 +296,20 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, int tpt, Paged
   return true;
 }
 
-// Header of a CTA that leaves the item of piece c unfinished: the CTAs from this one on that
-// hold its parts, and where its rows go.  {parts, tile head, first token, tokens}.  Called by the
-// thread that wrote the empty header.
+// The CTA whose share holds place x of the line.
+__device__ __forceinline__ int paged_cta_of(const PagedSched& s, long long x) {
+  return static_cast<int>(((x + 1) * s.ctas + s.W - 1) / s.W) - 1;
+}
+
+// Header of a piece c that is not a whole item, in its slot: {first CTA of the item's parts, their
+// number << 16 | tokens, tile head, first token}.  Called by the thread that wrote the empty one.
 template <int C>
 __device__ __forceinline__ void paged_header(const PagedParams& p, const PagedSched& s,
-                                             const PagedRec& r, int h, int cta) {
-  const long long end = r.lin + static_cast<long long>(h) * (r.n + C) + r.n;  // of its tiles
-  const long long last = (end * s.ctas + s.W - 1) / s.W - 1;  // the CTA that reaches it
-  p.ws_head[cta] = make_int4(static_cast<int>(last - cta + 1), h, r.tok0, r.ntok);
+                                             const PagedRec& r, const PagedPiece& c, int cta) {
+  const long long start = r.lin + static_cast<long long>(c.h) * (r.n + C);
+  const int first = c.a == 0 ? cta : paged_cta_of(s, start);
+  const int last = c.b == r.n ? cta : paged_cta_of(s, start + r.n - 1);
+  p.ws_head[paged_slot(cta, c)] = make_int4(first, (last - first + 1) << 16 | r.ntok, c.h, r.tok0);
 }
 
 // Natural-log log-sum-exp of a row from its maximum (log2 units) and sum; -inf without keys.
@@ -313,18 +318,31 @@ __device__ __forceinline__ float paged_lse(float m, float l) {
 }
 
 // ---------------------------------------------------------------------------------- join
-// Block (c, j) joins rows of the item that CTA c left unfinished: O = sum_i 2^(m_i - m) O_i / l,
-// l = sum_i 2^(m_i - m) l_i, over the parts in key order; part 0 is slot 1 of CTA c, part i slot 0
-// of CTA c + i.  Bound by the launch and two dependent loads (the header, the parts), as long as
-// the grid is about one wave and a warp has all its loads in flight; launched to overlap the end
-// of the kernel before.  Two forms:
-//   few rows, many parts (decoding): four warps share a row; each takes every fourth part, eight
-//     of them loaded at once, and they meet in warp order;
-//   many rows, two or three parts (chunks): each warp has four rows (eight where a row is 16
-//     lanes wide) in flight.  One row per warp and 32 blocks per item were 8 waves of blocks and
-//     40 us behind a 245 us kernel (8192 causal tokens, d = 128).
+// Rows of an item that several CTAs worked on: O = sum_i 2^(m_i - m) O_i / l,
+// l = sum_i 2^(m_i - m) l_i, over the parts in key order; part 0 is slot 1 of the first CTA, part i
+// slot 0 of the i-th behind it.  Bound by the launch, the dependent loads (the header, the parts)
+// and, after chunks, by the parts' 39 MB in L2 (148 SMs x two 128 KB parts); launched to overlap
+// the end of the kernel before.  Two forms:
+//   few rows, many parts (decoding): the blocks of the first CTA have all of them; four warps share
+//     a row, each takes every fourth part, eight of them loaded at once, and they meet in warp
+//     order;
+//   many rows (chunks): the blocks of each of an item's CTAs have an equal share of its rows, a row
+//     per group of lanes, four parts loaded at once.  (All rows by the first CTA's blocks: 45 us
+//     for 128 tokens over 2048 keys, 16 heads over 4, d = 64, whose items are in 9 parts; so 21.
+//     Several rows in flight per lane cost registers and were slower.)
 constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_ROWS = 4;  // rows in flight per group of lanes
+
+// The item of a header.
+struct PagedJoinItem {
+  int first, parts, rows, h, tok0;  // the CTAs that hold its parts; rows = 0: no item
+  __device__ __forceinline__ void get(const PagedParams& p, const int4& e) {
+    first = e.x;
+    parts = e.y >> 16;
+    rows = (e.y & 0xffff) * p.G;
+    h = e.z;
+    tok0 = e.w;
+  }
+};
 
 __device__ __forceinline__ size_t paged_part(int cta, int i) {
   return i == 0 ? static_cast<size_t>(cta) * 2 + 1 : static_cast<size_t>(cta + i) * 2;
@@ -356,29 +374,37 @@ struct PagedJoin {
   __device__ __forceinline__ void store(const PagedParams& p, long long row, int col) const {
     const float inv = l == 0.f ? 0.f : 1.0f / l;
     const float o[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-    T* op = static_cast<T*>(p.o) + row * p.d;
+    T* op = static_cast<T*>(p.o) + row * p.d + col;
+    if (p.d % 4 == 0) {  // o is 16-byte aligned
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+      else
+        *reinterpret_cast<float4*>(op) = make_float4(o[0], o[1], o[2], o[3]);
+    } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (col + c < p.d) op[col + c] = from_f<T>(o[c]);
+      for (int c = 0; c < 4; ++c)
+        if (col + c < p.d) op[c] = from_f<T>(o[c]);
+    }
     if (col == 0) p.lse[row] = paged_lse(m, l);
   }
 };
 
 template <typename T>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_few_kernel(const PagedParams p) {
-  constexpr int WPR = 4, DEPTH = 8;
-  __shared__ float4 s_acc[JOIN_WARPS][32];
-  __shared__ float2 s_ml[JOIN_WARPS];
   grid_dep_wait();
   grid_dep_launch();
   const int cta = blockIdx.x;
-  const int4 head = p.ws_head[cta];
-  if (head.x <= 0) return;
+  constexpr int WPR = 4, DEPTH = 8;
+  __shared__ float4 s_acc[JOIN_WARPS][32];
+  __shared__ float2 s_ml[JOIN_WARPS];
+  PagedJoinItem item;  // the one that the CTA leaves unfinished, if any
+  item.get(p, p.ws_head[2 * cta + 1]);
+  if (item.rows == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = head.w * p.G, parts = head.x;
+  const int rows = item.rows, parts = item.parts;
   for (int r0 = blockIdx.y * (JOIN_WARPS / WPR); r0 < rows; r0 += gridDim.y * (JOIN_WARPS / WPR)) {
     const int r = r0 + warp / WPR;
-    const int qh = paged_row_head(p, head.y, r, rows);
+    const int qh = paged_row_head(p, item.h, r, rows);
     PagedJoin j;
     for (int i0 = qh >= 0 ? warp % WPR : parts; i0 < parts; i0 += DEPTH * WPR) {
       float4 part[DEPTH];
@@ -403,14 +429,14 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_few_kernel(cons
     s_acc[warp][lane] = j.acc;
     if (lane == 0) s_ml[warp] = make_float2(j.m, j.l);
     __syncthreads();
-    if (warp % WPR == 0 && qh >= 0) {
+    if (warp % WPR == 0 && qh >= 0 && 4 * lane < p.d) {
       float top = j.m;
 #pragma unroll
       for (int w = 1; w < WPR; ++w) top = fmaxf(top, s_ml[warp + w].x);
       j.raise(top);
 #pragma unroll
       for (int w = 1; w < WPR; ++w) j.add(s_ml[warp + w], s_acc[warp + w][lane]);
-      j.store<T>(p, static_cast<long long>(head.z + r / p.G) * p.H + qh, 4 * lane);
+      j.store<T>(p, static_cast<long long>(item.tok0 + r / p.G) * p.H + qh, 4 * lane);
     }
     __syncthreads();  // s_acc is rewritten for the next rows
   }
@@ -419,48 +445,46 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_few_kernel(cons
 // LPR: lanes per row, 4 LPR >= d.
 template <typename T, int LPR>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) fa_paged_join_rows_kernel(const PagedParams p) {
-  constexpr int DEPTH = 2;
   grid_dep_wait();
   grid_dep_launch();
   const int cta = blockIdx.x;
-  const int4 head = p.ws_head[cta];
-  if (head.x <= 0) return;
-  const int rows = head.w * p.G, parts = head.x;
-  const int group = threadIdx.x / LPR, col = 4 * (threadIdx.x % LPR);
-  constexpr int GROUPS = JOIN_WARPS * 32 / LPR;
-  const int r0 = blockIdx.y * (GROUPS * JOIN_ROWS) + group;  // rows r0, r0 + GROUPS, ..
-  PagedJoin j[JOIN_ROWS];
-  for (int i0 = 0; i0 < parts; i0 += DEPTH) {
-    float4 part[JOIN_ROWS][DEPTH];
-    float2 ml[JOIN_ROWS][DEPTH];
+  constexpr int GROUPS = JOIN_WARPS * 32 / LPR, DEPTH = 4;
+  PagedJoinItem item[2];
+  int lo[2], n[2];  // this CTA's rows of the one item and of the other: n from lo on
 #pragma unroll
-    for (int k = 0; k < JOIN_ROWS; ++k)
+  for (int i = 0; i < 2; ++i) {
+    item[i].get(p, p.ws_head[2 * cta + i]);
+    const int rows = item[i].rows, parts = item[i].parts, at = cta - item[i].first;
+    lo[i] = parts == 0 ? 0 : rows * at / parts;
+    n[i] = parts == 0 ? 0 : rows * (at + 1) / parts - lo[i];
+  }
+  const int col = 4 * (threadIdx.x % LPR);
+  for (int e = blockIdx.y * GROUPS + threadIdx.x / LPR; e < n[0] + n[1]; e += gridDim.y * GROUPS) {
+    const bool second = e >= n[0];
+    const PagedJoinItem it = second ? item[1] : item[0];
+    const int row = second ? lo[1] + e - n[0] : lo[0] + e, first = it.first, parts = it.parts;
+    PagedJoin j;
+    for (int i0 = 0; i0 < parts; i0 += DEPTH) {
+      float4 part[DEPTH];
+      float2 ml[DEPTH];
+      float top = j.m;
 #pragma unroll
-      for (int e = 0; e < DEPTH; ++e) {
-        const int r = r0 + k * GROUPS;
-        ml[k][e] = make_float2(-INFINITY, 0.f);
-        part[k][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r >= rows || i0 + e >= parts) continue;
-        const size_t at = paged_part(cta, i0 + e) * p.rows_cap + r;
-        ml[k][e] = p.ws_ml[at];
-        if (col < p.d) part[k][e] = *reinterpret_cast<const float4*>(p.ws_o + at * p.ws_pitch + col);
+      for (int k = 0; k < DEPTH; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        part[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + k >= parts) continue;
+        const size_t at = paged_part(first, i0 + k) * p.rows_cap + row;
+        ml[k] = p.ws_ml[at];
+        if (col < p.d) part[k] = *reinterpret_cast<const float4*>(p.ws_o + at * p.ws_pitch + col);
       }
 #pragma unroll
-    for (int k = 0; k < JOIN_ROWS; ++k) {
-      float top = j[k].m;
+      for (int k = 0; k < DEPTH; ++k) top = fmaxf(top, ml[k].x);
+      j.raise(top);
 #pragma unroll
-      for (int e = 0; e < DEPTH; ++e) top = fmaxf(top, ml[k][e].x);
-      j[k].raise(top);
-#pragma unroll
-      for (int e = 0; e < DEPTH; ++e) j[k].add(ml[k][e], part[k][e]);
+      for (int k = 0; k < DEPTH; ++k) j.add(ml[k], part[k]);
     }
-  }
-#pragma unroll
-  for (int k = 0; k < JOIN_ROWS; ++k) {
-    const int r = r0 + k * GROUPS;
-    const int qh = paged_row_head(p, head.y, r, rows);
-    if (qh >= 0 && col < p.d)
-      j[k].store<T>(p, static_cast<long long>(head.z + r / p.G) * p.H + qh, col);
+    const int qh = paged_row_head(p, it.h, row, it.rows);
+    if (qh >= 0 && col < p.d) j.template store<T>(p, static_cast<long long>(it.tok0 + row / p.G) * p.H + qh, col);
   }
 }
 

@@ -89,7 +89,7 @@ size_t paged_ws_part(long long T, int group, int d, PagedShape v, int* rows_cap,
   const int splits = (group + v.rows - 1) / v.rows;
   const int G = (group + splits - 1) / splits;
   const long long cap = std::min<long long>(v.rows, T * G);
-  const size_t head = round256(static_cast<size_t>(v.ctas) * sizeof(int4));
+  const size_t head = round256(static_cast<size_t>(v.ctas) * 2 * sizeof(int4));
   const size_t ml = round256(static_cast<size_t>(v.ctas) * 2 * cap * sizeof(float2));
   if (rows_cap != nullptr) {
     *rows_cap = static_cast<int>(cap);
@@ -110,26 +110,27 @@ PagedShape f32_shape(int d) {
 PagedShape decode_shape() { return {16, kSms}; }
 PagedShape chunk_shape(int d) { return {256, kSms * (d == 64 ? fa::PagedChunkLayout<64>::CTAS_PER_SM : 1)}; }
 
+// The kernel of few rows per tile and that of many, as a call or a head dimension has them.
+template <typename T>
+PagedShape few_shape(int d) {
+  if constexpr (sizeof(T) == 2) return decode_shape();
+  else return f32_shape<fa::PagedF32Few>(d);
+}
+template <typename T>
+PagedShape many_shape(int d) {
+  if constexpr (sizeof(T) == 2) return chunk_shape(d);
+  else return f32_shape<fa::PagedF32Chunk>(d);
+}
+
 size_t paged_ws_bytes(long long T, int group, int d) {
   size_t n = 0;
-  for (const PagedShape v : {f32_shape<fa::PagedF32Few>(d), f32_shape<fa::PagedF32Chunk>(d), decode_shape(),
-                             chunk_shape(d)})
+  for (const PagedShape v : {few_shape<float>(d), many_shape<float>(d), few_shape<__nv_bfloat16>(d),
+                             many_shape<__nv_bfloat16>(d)})
     n = std::max(n, paged_ws_part(T, group, d, v, nullptr, nullptr, nullptr));
   return n;
 }
 
-// few: items have few rows (decoding).
-template <typename T>
-int launch_join(const fa::PagedParams& p, int ctas, bool few, cudaStream_t s) {
-  const int lpr = p.d <= 64 ? 16 : 32;
-  const int rows = few ? fa::JOIN_WARPS / 4 : fa::JOIN_WARPS * 32 / lpr * fa::JOIN_ROWS;  // of a block
-  auto* kern = few ? fa::fa_paged_join_few_kernel<T>
-                   : (lpr == 16 ? fa::fa_paged_join_rows_kernel<T, 16> : fa::fa_paged_join_rows_kernel<T, 32>);
-  return launch_overlapped("fa_paged_join_kernel", kern, dim3(ctas, (p.rows_cap + rows - 1) / rows),
-                           fa::JOIN_WARPS * 32, 0, s, p);
-}
-
-// Lays the workspace out for a variant and sets the tile fields of the parameters.
+// Sets the tile fields of a variant's parameters and lays its workspace out.
 void paged_tiles(fa::PagedParams& p, PagedShape v, int H_kv, void* ws) {
   size_t off_ml = 0, off_o = 0;
   p.splits = (p.group + v.rows - 1) / v.rows;
@@ -143,17 +144,22 @@ void paged_tiles(fa::PagedParams& p, PagedShape v, int H_kv, void* ws) {
   p.ws_o = reinterpret_cast<float*>(b + off_o);
 }
 
+// few: after the kernel of few rows per tile.
+template <typename T>
+int launch_join(const fa::PagedParams& p, int ctas, bool few, cudaStream_t s) {
+  // blocks per CTA: two rows each, or eight per SM
+  const int y = few ? (p.rows_cap + 1) / 2 : 8 * kSms / ctas;
+  auto* kern = few ? fa::fa_paged_join_few_kernel<T>
+                   : (p.d <= 64 ? fa::fa_paged_join_rows_kernel<T, 16> : fa::fa_paged_join_rows_kernel<T, 32>);
+  return launch_overlapped("fa_paged_join_kernel", kern, dim3(ctas, y), fa::JOIN_WARPS * 32, 0, s, p);
+}
+
 template <typename L>
-int launch_paged_f32(void (*kern)(fa::PagedParams), fa::PagedParams p, int H_kv, bool few, void* ws,
-                     cudaStream_t s) {
-  const PagedShape v = f32_shape<L>(p.d);
-  paged_tiles(p, v, H_kv, ws);
+int launch_paged_f32(void (*kern)(fa::PagedParams), const fa::PagedParams& p, cudaStream_t s) {
   const size_t smem = L::bytes(p.d);
-  int rc = set_smem(kern, static_cast<int>(smem));
+  const int rc = set_smem(kern, static_cast<int>(smem));
   if (rc != FA_OK) return rc;
-  rc = launch_overlapped("fa_paged_f32_kernel", kern, dim3(v.ctas), L::THREADS, smem, s, p);
-  if (rc != FA_OK) return rc;
-  return launch_join<float>(p, v.ctas, few, s);
+  return launch_overlapped("fa_paged_f32_kernel", kern, dim3(f32_shape<L>(p.d).ctas), L::THREADS, smem, s, p);
 }
 
 // 4-D view [page][H_kv][page_size][d] bf16 of a cache, 128-byte swizzled boxes of 64 columns and
@@ -179,23 +185,17 @@ int make_cache_map(CUtensorMap* map, const void* base, int pages, int H_kv, int 
 }
 
 template <int D>
-int launch_paged_decode(fa::PagedParams p, int H_kv, int page_size, void* ws, cudaStream_t s) {
+int launch_paged_decode(const fa::PagedParams& p, int H_kv, int page_size, cudaStream_t s) {
   using L = fa::PagedDecodeLayout<D>;
-  const PagedShape v = decode_shape();
-  paged_tiles(p, v, H_kv, ws);
   CUtensorMap mk, mv;
   const int box = std::min(page_size, L::KT);
   int rc;
   if ((rc = make_cache_map(&mk, p.k, p.num_pages, H_kv, page_size, D, p.k_page, box, "k_cache")) != FA_OK) return rc;
   if ((rc = make_cache_map(&mv, p.v, p.num_pages, H_kv, page_size, D, p.v_page, box, "v_cache")) != FA_OK) return rc;
   if ((rc = set_smem(fa::fa_paged_decode_sm100_kernel<D>, L::SMEM_ALLOC)) != FA_OK) return rc;
-  {
-    TimedLaunch tl("fa_paged_decode_sm100_kernel", s);
-    rc = launch_overlapped("fa_paged_decode_sm100_kernel", fa::fa_paged_decode_sm100_kernel<D>, dim3(v.ctas),
-                           L::THREADS, L::SMEM_ALLOC, s, mk, mv, p);
-    if (rc != FA_OK) return rc;
-  }
-  return launch_join<__nv_bfloat16>(p, v.ctas, true, s);
+  TimedLaunch tl("fa_paged_decode_sm100_kernel", s);
+  return launch_overlapped("fa_paged_decode_sm100_kernel", fa::fa_paged_decode_sm100_kernel<D>,
+                           dim3(decode_shape().ctas), L::THREADS, L::SMEM_ALLOC, s, mk, mv, p);
 }
 
 // 3-D view [T][H][d] bf16 of the packed queries, 128-byte swizzled boxes of 64 columns, `heads`
@@ -218,10 +218,8 @@ int make_query_map(CUtensorMap* map, const fa::PagedParams& p, int heads, int to
 }
 
 template <int D>
-int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cudaStream_t s) {
+int launch_paged_chunk(const fa::PagedParams& p, int H_kv, int page_size, cudaStream_t s) {
   using L = fa::PagedChunkLayout<D>;
-  const PagedShape v = chunk_shape(D);
-  paged_tiles(p, v, H_kv, ws);
   CUtensorMap mq, mqf, mk, mv;
   const int box = std::min(page_size, L::BN);
   const int tpt = L::R / p.G, few = std::min(tpt, std::max(1, 32 / p.G));
@@ -231,13 +229,9 @@ int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cud
   if ((rc = make_cache_map(&mk, p.k, p.num_pages, H_kv, page_size, D, p.k_page, box, "k_cache")) != FA_OK) return rc;
   if ((rc = make_cache_map(&mv, p.v, p.num_pages, H_kv, page_size, D, p.v_page, box, "v_cache")) != FA_OK) return rc;
   if ((rc = set_smem(fa::fa_paged_chunk_sm100_kernel<D>, L::SMEM_ALLOC)) != FA_OK) return rc;
-  {
-    TimedLaunch tl("fa_paged_chunk_sm100_kernel", s);
-    rc = launch_overlapped("fa_paged_chunk_sm100_kernel", fa::fa_paged_chunk_sm100_kernel<D>, dim3(v.ctas),
-                           L::THREADS, L::SMEM_ALLOC, s, mq, mqf, mk, mv, few, p);
-    if (rc != FA_OK) return rc;
-  }
-  return launch_join<__nv_bfloat16>(p, v.ctas, false, s);
+  TimedLaunch tl("fa_paged_chunk_sm100_kernel", s);
+  return launch_overlapped("fa_paged_chunk_sm100_kernel", fa::fa_paged_chunk_sm100_kernel<D>,
+                           dim3(chunk_shape(D).ctas), L::THREADS, L::SMEM_ALLOC, s, mq, mqf, mk, mv, few, p);
 }
 
 // Rows of a K/V head (tokens x heads of its group) up to which the kernels of few rows per tile run;
@@ -251,6 +245,40 @@ int launch_paged_chunk(fa::PagedParams p, int H_kv, int page_size, void* ws, cud
 long long few_rows(int dtype, long long keys) {
   if (dtype == FA_F32) return 24;
   return keys <= 8ll * 64 * kSms ? 48 : 16;
+}
+
+// The kernel of few rows per tile (few) or of many.
+template <typename T>
+int launch_paged(bool few, const fa::PagedParams& p, int H_kv, int page_size, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (few)
+      return p.d == 64 ? launch_paged_decode<64>(p, H_kv, page_size, s) : launch_paged_decode<128>(p, H_kv, page_size, s);
+    return p.d == 64 ? launch_paged_chunk<64>(p, H_kv, page_size, s) : launch_paged_chunk<128>(p, H_kv, page_size, s);
+  } else {
+    using Kernel = void (*)(fa::PagedParams);
+    const int nc = (p.d - 1) / 32;
+    if (few) {
+      const Kernel kernels[4] = {fa::fa_paged_f32_few_kernel<1>, fa::fa_paged_f32_few_kernel<2>,
+                                 fa::fa_paged_f32_few_kernel<3>, fa::fa_paged_f32_few_kernel<4>};
+      return launch_paged_f32<fa::PagedF32Few>(kernels[nc], p, s);
+    }
+    const Kernel kernels[4] = {fa::fa_paged_f32_chunk_kernel<1>, fa::fa_paged_f32_chunk_kernel<2>,
+                               fa::fa_paged_f32_chunk_kernel<3>, fa::fa_paged_f32_chunk_kernel<4>};
+    return launch_paged_f32<fa::PagedF32Chunk>(kernels[nc], p, s);
+  }
+}
+
+// The kernel that suits the batch, and its join.  room: K/V heads x positions that the batch's block
+// table has room for.
+template <typename T>
+int paged_run(fa::PagedParams p, int max_q, long long room, int H_kv, int page_size, void* ws, cudaStream_t s) {
+  // new tokens of a request: the caller's bound, or the mean
+  const long long most = max_q > 0 ? std::min(max_q, p.T) : (static_cast<long long>(p.T) + p.B - 1) / p.B;
+  const bool few = most * p.group <= few_rows(sizeof(T) == 2 ? FA_BF16 : FA_F32, room);
+  const PagedShape v = few ? few_shape<T>(p.d) : many_shape<T>(p.d);
+  paged_tiles(p, v, H_kv, ws);
+  const int rc = launch_paged<T>(few, p, H_kv, page_size, s);
+  return rc != FA_OK ? rc : launch_join<T>(p, v.ctas, few, s);
 }
 
 // Whether [a, a + an) and [b, b + bn) share a byte.
@@ -566,26 +594,9 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
   p.causal = causal ? 1 : 0;
   p.scale2 = scale * kLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // new tokens per request: the caller's bound, or the batch's mean
-  const long long rows = static_cast<long long>(max_q > 0 ? std::min(max_q, T) : (T + B - 1) / B) * p.group;
-  const bool few = rows <= few_rows(dtype, static_cast<long long>(B) * H_kv * (max_pages << shift));
-  if (dtype == FA_BF16) {
-    if (few)
-      return d == 64 ? launch_paged_decode<64>(p, H_kv, page_size, workspace, s)
-                     : launch_paged_decode<128>(p, H_kv, page_size, workspace, s);
-    return d == 64 ? launch_paged_chunk<64>(p, H_kv, page_size, workspace, s)
-                   : launch_paged_chunk<128>(p, H_kv, page_size, workspace, s);
-  }
-  using Kernel = void (*)(fa::PagedParams);
-  const int nc = (d - 1) / 32;
-  if (few) {
-    const Kernel kernels[4] = {fa::fa_paged_f32_few_kernel<1>, fa::fa_paged_f32_few_kernel<2>,
-                               fa::fa_paged_f32_few_kernel<3>, fa::fa_paged_f32_few_kernel<4>};
-    return launch_paged_f32<fa::PagedF32Few>(kernels[nc], p, H_kv, true, workspace, s);
-  }
-  const Kernel kernels[4] = {fa::fa_paged_f32_chunk_kernel<1>, fa::fa_paged_f32_chunk_kernel<2>,
-                             fa::fa_paged_f32_chunk_kernel<3>, fa::fa_paged_f32_chunk_kernel<4>};
-  return launch_paged_f32<fa::PagedF32Chunk>(kernels[nc], p, H_kv, false, workspace, s);
+  const long long room = static_cast<long long>(B) * H_kv * (max_pages << shift);
+  return dtype == FA_BF16 ? paged_run<__nv_bfloat16>(p, max_q, room, H_kv, page_size, workspace, s)
+                          : paged_run<float>(p, max_q, room, H_kv, page_size, workspace, s);
 }
 
 int fa_rope_packed(const fa_rope_args* args) {

@@ -41,6 +41,9 @@ struct PagedChunkLayout {
   static constexpr int R = 256;
   static constexpr int BN = D == 64 ? 64 : 128;     // keys per tile
   static constexpr int C = 3;                       // an item's constant, in key tiles
+  // key tiles that are worth a CTA: 128 tokens over 2048 keys, 16 heads over 4, d = 64 (128): 27 (23) us
+  // with 1, 22 (26) with 4, 29 (36) with 8
+  static constexpr int LEAST = BN == 64 ? 4 : 1;
   static constexpr int CTAS_PER_SM = BN == 64 ? 2 : 1;
   static constexpr int THREADS = 320;
   static constexpr int KST = BN == 64 ? 4 : 3;      // K ring depth
@@ -145,7 +148,7 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
   const int cta = blockIdx.x;
   long long x, hi;
   PagedMine mine = {};
-  if (!paged_share<BN, C, 320>(p, tpt, sched, x, hi, mine)) return;
+  if (!paged_share<BN, C, 320, L::LEAST>(p, tpt, sched, x, hi, mine)) return;
   if (threadIdx.x == 0) {
     mbar_init(bar_qf, 1);
     mbar_init(bar_qe, 1);
@@ -551,7 +554,7 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           }
           tc_fence_before();  // O has been read before this warpgroup's next P goes out
         }
-        if (threadIdx.x == 0 && c.a == 0 && c.b < rc.n) paged_header<C>(p, sched, rc, c.h, cta);
+        if (threadIdx.x == 0 && !whole) paged_header<C>(p, sched, rc, pc, cta);
       }
     }
     x = stop;

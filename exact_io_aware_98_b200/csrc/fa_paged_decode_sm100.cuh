@@ -403,7 +403,7 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
           }
           named_bar_sync(1, L::WARPS * 32);  // s_o (and, after the last, s_ml and Q) may be rewritten
         }
-        if (tid == 0 && pc.a == 0 && pc.b < rc.n) paged_header<C>(p, sched, rc, pc.h, cta);
+        if (tid == 0 && !whole) paged_header<C>(p, sched, rc, pc, cta);
       }
     }
     x = stop;

@@ -248,6 +248,7 @@ fa_paged_f32_few_kernel(const PagedParams p) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
 
+      const bool whole = pc.a == 0 && pc.b == rc.n;
       // join the key groups: their sums through the K tile's memory, statistics through P's
       float2* s_ml = reinterpret_cast<float2*>(s_p);  // [warps][RW]
       if (lane == 0)
@@ -268,7 +269,6 @@ fa_paged_f32_few_kernel(const PagedParams p) {
         const int first = r / RW * WK, in = r % RW;     // the row's warps, its row in them
         const int qh = paged_row_head(p, pc.h, r, rows);
         if (qh >= 0) {
-          const bool whole = pc.a == 0 && pc.b == rc.n;
           const size_t slot = paged_slot(cta, pc);
           float mm = -INFINITY, ll = 0.f, o[NC];
           for (int w = 0; w < WK; ++w) mm = fmaxf(mm, s_ml[(first + w) * RW + in].x);
@@ -293,7 +293,7 @@ fa_paged_f32_few_kernel(const PagedParams p) {
           }
         }
       }
-      if (tid == 0 && pc.a == 0 && pc.b < rc.n) paged_header<C>(p, sched, rc, pc.h, cta);
+      if (tid == 0 && !whole) paged_header<C>(p, sched, rc, pc, cta);
     }
     x = sched.stop;
     if (x >= hi) break;
@@ -466,7 +466,7 @@ fa_paged_f32_chunk_kernel(const PagedParams p) {
           else p.ws_ml[slot * p.rows_cap + r] = make_float2(m[i], l[i]);
         }
       }
-      if (tid == 0 && pc.a == 0 && pc.b < rc.n) paged_header<C>(p, sched, rc, pc.h, cta);
+      if (tid == 0 && !whole) paged_header<C>(p, sched, rc, pc, cta);
     }
     x = sched.stop;
     if (x >= hi) break;
