@@ -373,6 +373,7 @@ int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t*
   if (shift < 0) return fail(FA_ERR_INVALID, "page_size must be a power of two in [16, 1024], got %d", page_size);
   if (B < 1 || max_pages < 1 || max_tokens < 1 || n_free < 0)
     return fail(FA_ERR_INVALID, "B, max_pages, max_tokens >= 1 and n_free >= 0 required");
+  if (B > (1 << 24) || max_tokens > (1 << 24)) return fail(FA_ERR_UNSUPPORTED, "B or max_tokens too large");
   if (!ctx_len || !new_len || (!free_pages && n_free > 0) || !block_table || !cu_q || !kv_len ||
       !positions || !slots || !counts)
     return fail(FA_ERR_INVALID, "null pointer");

@@ -226,6 +226,7 @@ int fa_rope(const void* x, void* y, const int32_t* positions, const double* inv_
  *   cu_q [B+1], kv_len [B], positions [max_tokens], slots [max_tokens] (int64), counts [4]:
  *       counts = {new tokens asked for, pages taken, pages short, cursor after}.
  *   No output may overlap an input (cursor = counts + 3, say: FA_ERR_INVALID); copy between steps.
+ *   B and max_tokens <= 2^24 (as T of the calls below).
  *   Tokens beyond max_tokens are left out of the step (of cu_q and kv_len as well).  A token whose
  *   page is missing (none left, or beyond max_pages, or a negative id) gets slot -1; an entry for
  *   which no page was left becomes -1.  Padding gets position 0, slot -1.

@@ -101,6 +101,12 @@ def test_workspace_size(lib):
     assert size(1 << 20, 8, 64, 1, 128) < 64 << 20  # bounded whatever the batch
 
 
+def test_plan_sizes_beyond_the_append(lib):
+    # as the append and the attention, which take 2^24 tokens; a block's token range then fits 32 bits
+    assert _plan(lib, cap=(1 << 24) + 1) == UNSUPPORTED and _plan(lib, cap=0x7fffffff) == UNSUPPORTED
+    assert _plan(lib, B=(1 << 24) + 1) == UNSUPPORTED
+
+
 def test_plan_reference_by_hand():
     """ctx 17 (pages 5, 6), 3 new: rows 1-3 of page 6.  ctx 0, 18 new: pages 9 and 2."""
     table = np.array([[5, 6, -1], [-1, -1, -1]], np.int32)
