@@ -5,14 +5,16 @@
 // Bound by HBM: K and V are read once.  The loop therefore is a stream: four producer warps keep a
 // ring of 64-key K/V tiles filled by TMA (one box per page and 64 columns; 128-byte swizzle; a
 // warp issues its boxes one after the other, so 16-row pages want several warps: 3.9 TB/s with
-// one, 4.6 with two, 5.0 with four at d = 64),
-// and eight consumer warps, in two groups that take alternate tiles, work on 16 keys each with
-// warp-level m16n8k16 MMAs -- the 16 rows fill one such tile, where a tcgen05 tile would be 128
-// rows of which 112 are idle, and the S and P of a warp never leave its registers.  Each warp
-// keeps its own running maximum and sum, so warps meet once per item, not per tile; the eight
-// partial results are then added through shared memory in fp32.  An SM has about 22 bytes of HBM
-// per cycle, a 64-key tile (d = 128) takes 1490 cycles to arrive, and a group needs about 500
-// for it, so the stream, not the arithmetic, sets the pace.
+// one, 4.6 with two, 5.0 with four at d = 64), and eight consumer warps, in two groups that take
+// alternate tiles, work on 16 keys each with warp-level m16n8k16 MMAs -- the 16 rows fill one such
+// tile, where a tcgen05 tile would be 128 rows of which 112 are idle, and the S and P of a warp
+// never leave its registers.  Each warp keeps its own running maximum and sum, so warps meet once
+// per item, not per tile; the eight partial results are then added through shared memory in fp32.
+// An SM has about 22 bytes of HBM per cycle, a 64-key tile (d = 128) takes 1490 cycles to arrive,
+// and a group needs about 500 for it, so the stream, not the arithmetic, sets the pace.
+// Measured: 64 requests of up to 16384 keys, 32 heads over 8, d = 128 (2.17 GB): 335 us, 6.5 TB/s,
+// the rate of a copy; 16 requests of 8192 keys: 91 us, 5.9 TB/s (d = 128), 51 us, 5.2 TB/s (d = 64);
+// one request of 2000 keys: 10 us with its join.
 //
 // Page ids are fetched 8 to 32 tiles ahead.  A page that the table does not name, or that lies behind
 // the last key, is read as an out-of-range page, which TMA fills with zeros without reading.

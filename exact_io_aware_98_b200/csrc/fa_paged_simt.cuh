@@ -9,7 +9,7 @@
 //   fa_paged_f32_few_kernel (8 rows, 128 keys a tile, 8 warps): few rows per K/V head (decoding).
 //     Warps in 2 row groups x 4 key groups, 4 rows and 32 keys each; lane = key for the scores, for
 //     P V a lane has the columns lane, lane + 32, ..  Bound by HBM: 16 requests of 8192 keys, 8
-//     heads over 2, take 104 us (2.6 TB/s) at d 128.
+//     heads over 2, take 102 us (2.6 TB/s) at d 128.
 //   fa_paged_f32_chunk_kernel (64 rows, 64 keys a tile, 256 threads): a thread forms 4 rows x 4 keys
 //     of scores and 4 rows x 2 NC columns of O, so that a value read from shared memory enters four
 //     products.  512 tokens over 8192 keys, 16 heads over 4, d 128: 1.07 ms, 32 TFLOP/s (a lane
