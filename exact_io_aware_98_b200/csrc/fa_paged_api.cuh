@@ -110,22 +110,10 @@ PagedShape f32_shape(int d) {
 PagedShape decode_shape() { return {16, kSms}; }
 PagedShape chunk_shape(int d) { return {256, kSms * (d == 64 ? fa::PagedChunkLayout<64>::CTAS_PER_SM : 1)}; }
 
-// The kernel of few rows per tile and that of many, as a call or a head dimension has them.
-template <typename T>
-PagedShape few_shape(int d) {
-  if constexpr (sizeof(T) == 2) return decode_shape();
-  else return f32_shape<fa::PagedF32Few>(d);
-}
-template <typename T>
-PagedShape many_shape(int d) {
-  if constexpr (sizeof(T) == 2) return chunk_shape(d);
-  else return f32_shape<fa::PagedF32Chunk>(d);
-}
-
 size_t paged_ws_bytes(long long T, int group, int d) {
   size_t n = 0;
-  for (const PagedShape v : {few_shape<float>(d), many_shape<float>(d), few_shape<__nv_bfloat16>(d),
-                             many_shape<__nv_bfloat16>(d)})
+  for (const PagedShape v : {f32_shape<fa::PagedF32Few>(d), f32_shape<fa::PagedF32Chunk>(d), decode_shape(),
+                             chunk_shape(d)})
     n = std::max(n, paged_ws_part(T, group, d, v, nullptr, nullptr, nullptr));
   return n;
 }
@@ -234,51 +222,38 @@ int launch_paged_chunk(const fa::PagedParams& p, int H_kv, int page_size, cudaSt
                            dim3(chunk_shape(D).ctas), L::THREADS, L::SMEM_ALLOC, s, mq, mqf, mk, mv, few, p);
 }
 
-// Rows of a K/V head (tokens x heads of its group) up to which the kernels of few rows per tile run;
-// keys: K/V heads x positions that the batch's block table has room for.
+// Rows of a K/V head (new tokens x heads of its group) up to which the kernels of few rows per tile run.
 //   bf16: 16 rows, one tile.  More rows read the cache once per tile: 16 requests of 8192 keys, 32
-//   heads over 8, d 128, take 93 us with 16 rows (chunk kernel 117), 172 with 24 (116).  Where
-//   the whole cache is eight 64-key tiles per SM or less, a call is latency and not bytes, and
-//   the few-row kernel has less of it: 2 requests of 2048 keys, 48 rows: 20 us against 23.
-//   fp32: 24 rows, three tiles of 8: 4 requests of 4096 keys, 8 heads over 4, d 128: 35 us with 8
-//   rows (chunk kernel 85), 59 with 16 (87), 78 with 24 (89), 101 with 32 (91).
-long long few_rows(int dtype, long long keys) {
-  if (dtype == FA_F32) return 24;
-  return keys <= 8ll * 64 * kSms ? 48 : 16;
-}
+//   heads over 8, d 128, take 98 us with 16 rows (chunk kernel 112), 177 with 24 (112); 2 requests
+//   of 2048 keys 16 us (17) and 19 (17).
+//   fp32: 24 rows, three tiles of 8: 4 requests of 4096 keys, 8 heads over 4, d 128: 36 us with 8
+//   rows (chunk kernel 83), 60 with 16 (84), 79 with 24 (85), 103 with 32 (86).
+int few_rows(int dtype) { return dtype == FA_F32 ? 24 : 16; }
 
-// The kernel of few rows per tile (few) or of many.
-template <typename T>
-int launch_paged(bool few, const fa::PagedParams& p, int H_kv, int page_size, cudaStream_t s) {
-  if constexpr (sizeof(T) == 2) {
-    if (few)
-      return p.d == 64 ? launch_paged_decode<64>(p, H_kv, page_size, s) : launch_paged_decode<128>(p, H_kv, page_size, s);
-    return p.d == 64 ? launch_paged_chunk<64>(p, H_kv, page_size, s) : launch_paged_chunk<128>(p, H_kv, page_size, s);
-  } else {
-    using Kernel = void (*)(fa::PagedParams);
-    const int nc = (p.d - 1) / 32;
-    if (few) {
-      const Kernel kernels[4] = {fa::fa_paged_f32_few_kernel<1>, fa::fa_paged_f32_few_kernel<2>,
-                                 fa::fa_paged_f32_few_kernel<3>, fa::fa_paged_f32_few_kernel<4>};
-      return launch_paged_f32<fa::PagedF32Few>(kernels[nc], p, s);
-    }
-    const Kernel kernels[4] = {fa::fa_paged_f32_chunk_kernel<1>, fa::fa_paged_f32_chunk_kernel<2>,
-                               fa::fa_paged_f32_chunk_kernel<3>, fa::fa_paged_f32_chunk_kernel<4>};
-    return launch_paged_f32<fa::PagedF32Chunk>(kernels[nc], p, s);
-  }
-}
-
-// The kernel that suits the batch, and its join.  room: K/V heads x positions that the batch's block
-// table has room for.
-template <typename T>
-int paged_run(fa::PagedParams p, int max_q, long long room, int H_kv, int page_size, void* ws, cudaStream_t s) {
-  // new tokens of a request: the caller's bound, or the mean
-  const long long most = max_q > 0 ? std::min(max_q, p.T) : (static_cast<long long>(p.T) + p.B - 1) / p.B;
-  const bool few = most * p.group <= few_rows(sizeof(T) == 2 ? FA_BF16 : FA_F32, room);
-  const PagedShape v = few ? few_shape<T>(p.d) : many_shape<T>(p.d);
+// The kernel of the batch and its join; rows: of a K/V head.
+int paged_run_bf16(fa::PagedParams p, long long rows, int H_kv, int page_size, void* ws, cudaStream_t s) {
+  const bool few = rows <= few_rows(FA_BF16);
+  const PagedShape v = few ? decode_shape() : chunk_shape(p.d);
   paged_tiles(p, v, H_kv, ws);
-  const int rc = launch_paged<T>(few, p, H_kv, page_size, s);
-  return rc != FA_OK ? rc : launch_join<T>(p, v.ctas, few, s);
+  int rc;
+  if (few) rc = p.d == 64 ? launch_paged_decode<64>(p, H_kv, page_size, s) : launch_paged_decode<128>(p, H_kv, page_size, s);
+  else rc = p.d == 64 ? launch_paged_chunk<64>(p, H_kv, page_size, s) : launch_paged_chunk<128>(p, H_kv, page_size, s);
+  return rc != FA_OK ? rc : launch_join<__nv_bfloat16>(p, v.ctas, few, s);
+}
+
+int paged_run_f32(fa::PagedParams p, long long rows, int H_kv, void* ws, cudaStream_t s) {
+  using Kernel = void (*)(fa::PagedParams);
+  const bool few = rows <= few_rows(FA_F32);
+  const PagedShape v = few ? f32_shape<fa::PagedF32Few>(p.d) : f32_shape<fa::PagedF32Chunk>(p.d);
+  paged_tiles(p, v, H_kv, ws);
+  const Kernel few_kernels[4] = {fa::fa_paged_f32_few_kernel<1>, fa::fa_paged_f32_few_kernel<2>,
+                                 fa::fa_paged_f32_few_kernel<3>, fa::fa_paged_f32_few_kernel<4>};
+  const Kernel chunk_kernels[4] = {fa::fa_paged_f32_chunk_kernel<1>, fa::fa_paged_f32_chunk_kernel<2>,
+                                   fa::fa_paged_f32_chunk_kernel<3>, fa::fa_paged_f32_chunk_kernel<4>};
+  const int nc = (p.d - 1) / 32;
+  const int rc = few ? launch_paged_f32<fa::PagedF32Few>(few_kernels[nc], p, s)
+                     : launch_paged_f32<fa::PagedF32Chunk>(chunk_kernels[nc], p, s);
+  return rc != FA_OK ? rc : launch_join<float>(p, v.ctas, few, s);
 }
 
 // Whether [a, a + an) and [b, b + bn) share a byte.
@@ -595,9 +570,11 @@ int fa_paged_fwd(const void* q, const void* k_cache, const void* v_cache,
   p.causal = causal ? 1 : 0;
   p.scale2 = scale * kLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const long long room = static_cast<long long>(B) * H_kv * (max_pages << shift);
-  return dtype == FA_BF16 ? paged_run<__nv_bfloat16>(p, max_q, room, H_kv, page_size, workspace, s)
-                          : paged_run<float>(p, max_q, room, H_kv, page_size, workspace, s);
+  // new tokens of a request: the caller's bound, or the mean
+  const long long most = max_q > 0 ? std::min(max_q, T) : (static_cast<long long>(T) + B - 1) / B;
+  const long long rows = most * p.group;
+  return dtype == FA_BF16 ? paged_run_bf16(p, rows, H_kv, page_size, workspace, s)
+                          : paged_run_f32(p, rows, H_kv, workspace, s);
 }
 
 int fa_rope_packed(const fa_rope_args* args) {

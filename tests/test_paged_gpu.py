@@ -561,3 +561,44 @@ def test_served_steps_match_dense_attention(cuda_lib, dtype, d):
         tol = 2 * 2.0 ** -8 * (av + o.float().abs()) if dtype == "bf16" else torch.full_like(av, 1e-5)
         assert torch.all((mine_o.float() - o.float()).abs() <= tol + 1e-6)
         assert (mine_l - lse).abs().max() <= 1e-3 if dtype == "bf16" else 1e-5
+
+
+# ------------- 17 to 32 rows of a K/V head: more than the decoding kernel's, few for the chunk kernel
+FEW = [(1, 1), (2, 2), (3, 64), (5, 65), (8, 700), (7, 3), (4, 0), (0, 9), (1, 2049), (8, 128), (6, 6)]
+BETWEEN = [
+    # lens, H, H_kv, d, page, causal, max_q
+    (FEW, 8, 2, 128, 16, True, 8),                      # 32 rows
+    (FEW, 8, 2, 64, 32, False, 8),
+    (FEW, 6, 2, 128, 64, True, 8),                      # three heads a group, 24 rows
+    (FEW, 10, 2, 64, 16, True, 4),                      # five: 20 rows
+    (DECODE, 32, 1, 128, 16, True, 1),                  # 32 heads a group
+    (DECODE, 40, 2, 64, 64, True, 1),                   # 20
+    (DECODE, 17, 1, 128, 128, False, 1),                # 17
+    (RAGGED, 4, 1, 64, 16, True, 5),                    # longer than the hint
+    (RAGGED, 3, 1, 128, 32, True, 6),
+    ([(8, 20000)] * 6, 8, 2, 128, 64, True, 8),         # the ring goes round
+    ([(6, 30000), (1, 70)] * 5, 8, 2, 64, 16, True, 6),
+    ([(2, 9000), (1, 1)] * 9, 36, 2, 128, 32, True, 1),
+    ([(5, 300), (1, 7)] * 300, 4, 1, 64, 16, True, 5),  # many small requests
+    ([(1, 3), (7, 7), (0, 7)] * 3000, 3, 1, 128, 16, True, 7),
+]
+
+
+@pytest.mark.parametrize("case", range(len(BETWEEN)))
+def test_paged_attention_between_the_kernels(cuda_lib, case):
+    lens, H, H_kv, d, page, causal, max_q = BETWEEN[case]
+    assert 16 < max_q * (H // H_kv) <= 32
+    c = paged_case(lens, H, H_kv, d, page, "bf16", seed=100 + case)
+    _, o, lse, o0, l0, scale = _run(cuda_lib, c, causal, max_q)
+    check_paged(c, o, lse, causal, scale, o_before=o0, lse_before=l0)
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+def test_between_the_kernels_as_the_others(cuda_lib, d, page):
+    """Two heads a group and a hint of 12 new tokens: 24 rows."""
+    test_bad_pages_are_masked(cuda_lib, "bf16", d, page, 12)
+    test_paged_layouts_and_large_scores(cuda_lib, "bf16", d, 12)
+    test_outputs_at_any_allowed_alignment(cuda_lib, "bf16", d, 12)
+    test_a_bad_request_stays_alone(cuda_lib, "bf16", d, 12)
+    test_offsets_beyond_32_bits(cuda_lib, "bf16", d, 12)
+    test_lengths_out_of_range_are_clamped(cuda_lib, 12)
