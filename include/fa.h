@@ -263,7 +263,8 @@ size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d);
  * in fa_fwd_gqa: O = softmax(scale Q K^T, masked) V and lse, decoding steps and prompt chunks in
  * any mix.
  *   q [T][H][d] (positive token and head strides in elements), o [T][H][d] and lse [T][H]
- *   contiguous; the three may not overlap, and neither may the workspace overlap anything.
+ *   contiguous; the three may not overlap, and neither may the workspace overlap anything.  q, the
+ *   caches, o and lse must be 16-byte aligned.
  *   Masks      token i of a request with nq new tokens sees the keys j < kv_len[b] with, causal
  *              != 0, j <= kv_len[b] - nq + i.  A key whose block-table entry is outside
  *              [0, num_pages) is masked.  A row with no key gets O = 0, lse = -inf.  What stale
