@@ -11,11 +11,12 @@
 //     P V a lane has the columns lane, lane + 32, ..  Bound by HBM: 16 requests of 8192 keys, 8
 //     heads over 2, take 102 us (2.6 TB/s) at d 128.
 //   fa_paged_f32_chunk_kernel (64 rows, 64 keys a tile, 256 threads): a thread forms 4 rows x 4 keys
-//     of scores and 4 rows x 2 NC columns of O, so that a value read from shared memory enters four
-//     products.  512 tokens over 8192 keys, 16 heads over 4, d 128: 1.07 ms, 32 TFLOP/s (a lane
-//     per key with Q broadcast, 32 rows a tile: 1.16 ms).  Neither FFMA (35 % of its slots) nor
-//     shared memory (57 %) is full: with one or two blocks per SM, latencies between the phases of
-//     a tile remain; unrolling the score loop or leaving its packed FMA out changed nothing.
+//     of scores and 4 rows x 2 NC columns of O (in pairs: one 8-byte read of V, packed FMAs), so
+//     that a value read from shared memory enters four products.  512 tokens over 8192 keys, 16
+//     heads over 4, d 128: 1.01 ms, 34 TFLOP/s (single columns 16 apart: 1.07 ms; a lane per key
+//     with Q broadcast, 32 rows a tile: 1.16 ms).  Neither FFMA (35 % of its slots) nor shared
+//     memory (57 %) is full: with one or two blocks per SM, latencies between the phases of a tile
+//     remain; unrolling the score loop or leaving its packed FMA out changed nothing.
 #pragma once
 #include "fa_paged.cuh"
 
@@ -317,7 +318,7 @@ fa_paged_f32_chunk_kernel(const PagedParams p) {
   long long* s_off = reinterpret_cast<long long*>(s_p + KT * L::P_PITCH);
   PagedSched& sched = *reinterpret_cast<PagedSched*>(s_off + 6 * KT);
   const int tid = threadIdx.x;
-  const int tx = tid & 15, ty = tid >> 4;  // keys tx + 16 k and columns tx + 16 c; rows 4 ty + i
+  const int tx = tid & 15, ty = tid >> 4;  // keys tx + 16 k, columns 32 c + 2 tx and the next; rows 4 ty + i
   const int tpt = R / p.G;  // G <= R
 
   // zero the columns that pad d up to a multiple of 4 (read by the 16-byte accesses)
@@ -431,14 +432,15 @@ fa_paged_f32_chunk_kernel(const PagedParams p) {
 #pragma unroll 4
         for (int kk = 0; kk < KT; ++kk) {
           const float4 pr = *reinterpret_cast<const float4*>(s_p + kk * L::P_PITCH + 4 * ty);
-          const float* vr = s_v + kk * pitch + tx;  // columns from d on: other values, never written out
+          const float* vr = s_v + kk * pitch + 2 * tx;  // columns from d on: other values, never written out
 #pragma unroll
-          for (int c = 0; c < CO; ++c) {
-            const float v = vr[16 * c];
-            acc[0][c] = fmaf(pr.x, v, acc[0][c]);
-            acc[1][c] = fmaf(pr.y, v, acc[1][c]);
-            acc[2][c] = fmaf(pr.z, v, acc[2][c]);
-            acc[3][c] = fmaf(pr.w, v, acc[3][c]);
+          for (int c = 0; c < CO; c += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(vr + 16 * c);
+            const float pi[4] = {pr.x, pr.y, pr.z, pr.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ffma2(acc[i][c], acc[i][c + 1], pi[i], pi[i], v.x, v.y, acc[i][c], acc[i][c + 1]);
+            }
           }
         }
         __syncthreads();  // V and P read
@@ -459,8 +461,10 @@ fa_paged_f32_chunk_kernel(const PagedParams p) {
         const long long row = static_cast<long long>(rc.tok0 + r / p.G) * p.H + qh;
         float* op = whole ? static_cast<float*>(p.o) + row * d : p.ws_o + (slot * p.rows_cap + r) * p.ws_pitch;
 #pragma unroll
-        for (int c = 0; c < CO; ++c)
-          if (16 * c + tx < d) op[16 * c + tx] = acc[i][c] * f;
+        for (int c = 0; c < CO; ++c) {
+          const int col = 16 * (c & ~1) + 2 * tx + (c & 1);
+          if (col < d) op[col] = acc[i][c] * f;
+        }
         if (tx == 0) {
           if (whole) p.lse[row] = paged_lse(m[i], l[i]);
           else p.ws_ml[slot * p.rows_cap + r] = make_float2(m[i], l[i]);
