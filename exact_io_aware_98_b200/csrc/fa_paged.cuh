@@ -313,6 +313,11 @@ __device__ __forceinline__ void paged_header(const PagedParams& p, const PagedSc
 }
 
 // Natural-log log-sum-exp of a row from its maximum (log2 units) and sum; -inf without keys.
+//
+// A sum is exactly 0 where a row saw no key, or only scores of -inf, and only there (else the key that
+// set the maximum has added 1).  So "no key" is read from the sum, never from the maximum: a row
+// whose scores are all NaN keeps the maximum -inf, which max passes NaN over, and its NaN is in the
+// sum.
 __device__ __forceinline__ float paged_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
@@ -362,8 +367,8 @@ struct PagedJoin {
     acc.w *= f;
   }
   __device__ __forceinline__ void add(float2 ml, float4 a) {  // ml.x <= m
-    if (ml.x == -INFINITY) return;
-    const float w = exp2f(ml.x - m);
+    if (ml.y == 0.f) return;  // no key
+    const float w = exp2f(ml.x - m);  // (NaN or 0 beside a NaN sum, which stays NaN)
     l = fmaf(w, ml.y, l);
     acc.x = fmaf(w, a.x, acc.x);
     acc.y = fmaf(w, a.y, acc.y);

@@ -344,8 +344,8 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
             float mm = -INFINITY;
 #pragma unroll
             for (int w = 0; w < L::WARPS; ++w) mm = fmaxf(mm, s_ml[w * L::R + r].x);
-            const float mine = half ? m1 : m0;
-            const float f = mine == -INFINITY ? 0.f : ex2_approx(mine - mm);
+            const bool some = (half ? l1 : l0) != 0.f;  // this warp has keys of the row
+            const float f = some ? ex2_approx((half ? m1 : m0) - mm) : 0.f;
             // group 1 hands over, group 0 adds its own (the same thread's places), row by row
             float* dst = s_o + (w4 * 8 + g) * L::PITCH + 2 * c;
             if (group == 1) {
@@ -376,7 +376,7 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
               for (int w = 0; w < L::WARPS; ++w) {
                 const float2 ml = s_ml[w * L::R + r];
-                if (ml.x != -INFINITY) ll = fmaf(ml.y, ex2_approx(ml.x - mm), ll);
+                if (ml.y != 0.f) ll = fmaf(ml.y, ex2_approx(ml.x - mm), ll);
               }
               constexpr int E = D / 32;  // columns of a lane
               float acc[E];

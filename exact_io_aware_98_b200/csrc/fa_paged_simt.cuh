@@ -259,7 +259,7 @@ fa_paged_f32_few_kernel(const PagedParams p) {
       for (int r = 0; r < RW; ++r) {
         float mm = -INFINITY;
         for (int w = 0; w < WK; ++w) mm = fmaxf(mm, s_ml[(wr * WK + w) * RW + r].x);
-        const float a = m[r] == -INFINITY ? 0.f : exp2f(m[r] - mm);
+        const float a = l[r] == 0.f ? 0.f : exp2f(m[r] - mm);
 #pragma unroll
         for (int c = 0; c < NC; ++c)  // never the padding columns, which stay zero
           if (32 * c + lane < d) s_k[(warp * RW + r) * pitch + 32 * c + lane] = acc[r][c] * a;
@@ -277,7 +277,7 @@ fa_paged_f32_few_kernel(const PagedParams p) {
           for (int c = 0; c < NC; ++c) o[c] = 0.f;
           for (int w = 0; w < WK; ++w) {
             const float2 ml = s_ml[(first + w) * RW + in];
-            if (ml.x != -INFINITY) ll = fmaf(ml.y, exp2f(ml.x - mm), ll);
+            if (ml.y != 0.f) ll = fmaf(ml.y, exp2f(ml.x - mm), ll);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
               if (32 * c + lane < d) o[c] += s_k[((first + w) * RW + in) * pitch + 32 * c + lane];

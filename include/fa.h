@@ -267,8 +267,10 @@ size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d);
  *   caches, o and lse must be 16-byte aligned.
  *   Masks      token i of a request with nq new tokens sees the keys j < kv_len[b] with, causal
  *              != 0, j <= kv_len[b] - nq + i.  A key whose block-table entry is outside
- *              [0, num_pages) is masked.  A row with no key gets O = 0, lse = -inf.  What stale
- *              rows of a page hold (NaN included) does not matter.
+ *              [0, num_pages) is masked.  A row with no key (or only scores of -inf) gets O = 0,
+ *              lse = -inf.  What stale rows of a page hold (NaN included) does not matter.
+ *   NaN        a row that sees a score of NaN gets NaN in O and lse, whatever the batch; other
+ *              rows do not notice.
  *   Lengths    cu_q is clamped to [0, T] and kv_len to [0, max_pages * page_size].  Rows of o
  *              and lse that no request owns are left as they were.
  *   max_q      the most new tokens of any request, as a hint for the choice of kernel only (every
