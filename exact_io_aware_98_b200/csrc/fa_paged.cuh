@@ -317,7 +317,8 @@ __device__ __forceinline__ void paged_header(const PagedParams& p, const PagedSc
 // A sum is exactly 0 where a row saw no key, or only scores of -inf, and only there (else the key that
 // set the maximum has added 1).  So "no key" is read from the sum, never from the maximum: a row
 // whose scores are all NaN keeps the maximum -inf, which max passes NaN over, and its NaN is in the
-// sum.
+// sum.  Where the sum is 0 the sums of P V count as 0 too, whatever they hold: 0 times a V that is
+// not finite is NaN.
 __device__ __forceinline__ float paged_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }

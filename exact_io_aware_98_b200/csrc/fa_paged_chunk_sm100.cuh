@@ -514,7 +514,7 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           const size_t slot = static_cast<size_t>(cta) * 2 + (c.a > 0 ? 0 : 1);
           const int qh = ok ? paged_row_head(p, c.h, r, rows) : -1;
           const long long row = static_cast<long long>(rc.tok0 + my_tok) * p.H + qh;
-          const float inv = l == 0.f ? 0.0f : 1.0f / l;
+          const float inv = 1.0f / l;
 #pragma unroll
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t o[32];
@@ -534,8 +534,9 @@ fa_paged_chunk_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
                   uint32_t hh[8];
 #pragma unroll
                   for (int e = 0; e < 8; ++e)
-                    hh[e] = pack_bf16x2(__uint_as_float(o[16 * i + 2 * e]) * inv,
-                                        __uint_as_float(o[16 * i + 2 * e + 1]) * inv);
+                    hh[e] = l == 0.f ? 0u
+                                     : pack_bf16x2(__uint_as_float(o[16 * i + 2 * e]) * inv,
+                                                   __uint_as_float(o[16 * i + 2 * e + 1]) * inv);
                   if (p.o_al32) {
                     st_global_256(dst + 16 * i, hh[0], hh[1], hh[2], hh[3], hh[4], hh[5], hh[6], hh[7]);
                   } else {

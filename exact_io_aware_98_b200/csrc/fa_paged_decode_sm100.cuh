@@ -345,17 +345,17 @@ fa_paged_decode_sm100_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int w = 0; w < L::WARPS; ++w) mm = fmaxf(mm, s_ml[w * L::R + r].x);
             const bool some = (half ? l1 : l0) != 0.f;  // this warp has keys of the row
-            const float f = some ? ex2_approx((half ? m1 : m0) - mm) : 0.f;
+            const float f = ex2_approx((half ? m1 : m0) - mm);
             // group 1 hands over, group 0 adds its own (the same thread's places), row by row
             float* dst = s_o + (w4 * 8 + g) * L::PITCH + 2 * c;
             if (group == 1) {
 #pragma unroll
               for (int i = 0; i < D / 8; ++i)
                 *reinterpret_cast<float2*>(dst + 8 * i) =
-                    make_float2(o[i][2 * half] * f, o[i][2 * half + 1] * f);
+                    some ? make_float2(o[i][2 * half] * f, o[i][2 * half + 1] * f) : make_float2(0.f, 0.f);
             }
             named_bar_sync(1, L::WARPS * 32);
-            if (group == 0) {
+            if (group == 0 && some) {
 #pragma unroll
               for (int i = 0; i < D / 8; ++i) {
                 const float2 other = *reinterpret_cast<const float2*>(dst + 8 * i);

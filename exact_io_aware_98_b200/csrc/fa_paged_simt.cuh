@@ -259,10 +259,11 @@ fa_paged_f32_few_kernel(const PagedParams p) {
       for (int r = 0; r < RW; ++r) {
         float mm = -INFINITY;
         for (int w = 0; w < WK; ++w) mm = fmaxf(mm, s_ml[(wr * WK + w) * RW + r].x);
-        const float a = l[r] == 0.f ? 0.f : exp2f(m[r] - mm);
+        const float a = exp2f(m[r] - mm);
 #pragma unroll
         for (int c = 0; c < NC; ++c)  // never the padding columns, which stay zero
-          if (32 * c + lane < d) s_k[(warp * RW + r) * pitch + 32 * c + lane] = acc[r][c] * a;
+          if (32 * c + lane < d)
+            s_k[(warp * RW + r) * pitch + 32 * c + lane] = l[r] == 0.f ? 0.f : acc[r][c] * a;
       }
       __syncthreads();
       {
@@ -463,7 +464,7 @@ fa_paged_f32_chunk_kernel(const PagedParams p) {
 #pragma unroll
         for (int c = 0; c < CO; ++c) {
           const int col = 16 * (c & ~1) + 2 * tx + (c & 1);
-          if (col < d) op[col] = acc[i][c] * f;
+          if (col < d) op[col] = l[i] == 0.f ? 0.f : acc[i][c] * f;
         }
         if (tx == 0) {
           if (whole) p.lse[row] = paged_lse(m[i], l[i]);

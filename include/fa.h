@@ -270,7 +270,8 @@ size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d);
  *              [0, num_pages) is masked.  A row with no key (or only scores of -inf) gets O = 0,
  *              lse = -inf.  What stale rows of a page hold (NaN included) does not matter.
  *   NaN        a row that sees a score of NaN gets NaN in O and lse, whatever the batch; other
- *              rows do not notice.
+ *              rows do not notice.  A V that is not finite reaches the rows that see its key; it may
+ *              also reach other rows of its request, if they have a key at all.
  *   Lengths    cu_q is clamped to [0, T] and kv_len to [0, max_pages * page_size].  Rows of o
  *              and lse that no request owns are left as they were.
  *   max_q      the most new tokens of any request, as a hint for the choice of kernel only (every

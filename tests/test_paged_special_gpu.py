@@ -82,6 +82,22 @@ def test_nan_keys(cuda_lib, dtype, d, max_q, first, last):
     _check(c, t, *_call(cuda_lib, t, max_q))
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,d,max_q", KERNELS)
+def test_rows_without_keys_beside_bad_values(cuda_lib, dtype, d, max_q, value):
+    """More new tokens than cached keys: the first rows see no key and are empty, although the values
+    that later rows of their tile see are not finite.  So is a part of which a row sees no key."""
+    c = paged_case([(6, 3), (70, 40), (300, 200), (9, 2)], 4, 2, d, 16, dtype, seed=51)
+    t = to_cuda(c)
+    t["v_cache"].fill_(value)
+    o, lse = _call(cuda_lib, t, max_q)
+    _check(c, t, o, lse)
+    at = 0
+    for nq, nk in c["lens"]:
+        assert torch.isfinite(lse[at + nq - nk:at + nq]).all() and not torch.isfinite(o[at + nq - 1]).any()
+        at += nq
+
+
 @pytest.mark.parametrize("dtype,d,max_q", KERNELS)
 def test_nan_does_not_depend_on_the_division(cuda_lib, dtype, d, max_q):
     """The same request alone and among 300 others: NaN in the same places."""
