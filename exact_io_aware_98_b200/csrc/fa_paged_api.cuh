@@ -361,7 +361,7 @@ int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t*
       !aligned_to(counts, 4))
     return fail(FA_ERR_ALIGN, "a pointer is not aligned to its elements");
   {
-    // blocks read the inputs while others write: an output must not be an input
+    // blocks read the inputs while others write: an output must not be an input, nor another output
     const size_t b4 = static_cast<size_t>(B) * 4, t4 = static_cast<size_t>(max_tokens) * 4;
     const size_t table_bytes = (static_cast<size_t>(B - 1) * (B > 1 ? table_stride : 0) + max_pages) * 4;
     const struct {
@@ -373,6 +373,9 @@ int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t*
       for (const auto& o : out)
         if (i.n > 0 && overlap(i.p, i.n, o.p, o.n))
           return fail(FA_ERR_INVALID, "an output overlaps an input");
+    for (int i = 0; i < 6; ++i)
+      for (int j = 0; j < i; ++j)
+        if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return fail(FA_ERR_INVALID, "two outputs overlap");
   }
   fa::PlanParams p;
   p.ctx_len = ctx_len;

@@ -225,7 +225,8 @@ int fa_rope(const void* x, void* y, const int32_t* positions, const double* inv_
  *                     in this step are written (ceil(ctx / page_size) on), the others are read.
  *   cu_q [B+1], kv_len [B], positions [max_tokens], slots [max_tokens] (int64), counts [4]:
  *       counts = {new tokens asked for, pages taken, pages short, cursor after}.
- *   No output may overlap an input (cursor = counts + 3, say: FA_ERR_INVALID); copy between steps.
+ *   No output may overlap an input (cursor = counts + 3, say) or another output: FA_ERR_INVALID; copy
+ *   between steps.
  *   B and max_tokens <= 2^24 (as T of the calls below).
  *   Tokens beyond max_tokens are left out of the step (of cu_q and kv_len as well).  A token whose
  *   page is missing (none left, or beyond max_pages, or a negative id) gets slot -1; an entry for
@@ -263,8 +264,8 @@ size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d);
  * in fa_fwd_gqa: O = softmax(scale Q K^T, masked) V and lse, decoding steps and prompt chunks in
  * any mix.
  *   q [T][H][d] (positive token and head strides in elements), o [T][H][d] and lse [T][H]
- *   contiguous; the three may not overlap, and neither may the workspace overlap anything.  q, the
- *   caches, o and lse must be 16-byte aligned.
+ *   contiguous; the three may not overlap (FA_ERR_INVALID).  Neither may o and lse overlap any other
+ *   input, nor the workspace anything.  q, the caches, o and lse must be 16-byte aligned.
  *   Masks      token i of a request with nq new tokens sees the keys j < kv_len[b] with, causal
  *              != 0, j <= kv_len[b] - nq + i.  A key whose block-table entry is outside
  *              [0, num_pages) is masked.  A row with no key (or only scores of -inf) gets O = 0,

@@ -52,6 +52,20 @@ def test_plan_codes(lib):
         assert "overlaps" in lib.fa_get_last_error().decode()
 
 
+def test_plan_outputs_apart(lib):
+    """Two outputs in one place would be written by different threads: refused, as an input is."""
+    base = dict(cu=A + 2048, kv=A + 2304, pos=A + 2560, slots=A + 4096, counts=A + 8192, tab=A + 1024)
+    size = dict(cu=12, kv=8, pos=16, slots=32, counts=16, tab=64)  # B = 2, 4 tokens, 8 pages a row
+    for a in base:
+        for b in base:
+            if a == b:
+                continue
+            step = 8 if b == "slots" else 4
+            for at in (base[a], base[a] + (size[a] - 1) // step * step):
+                assert _plan(lib, **{b: at}) == INVALID, (a, b)
+                assert "overlap" in lib.fa_get_last_error().decode()
+
+
 def _append(lib, q=A, k=A, qo=A + 4096, kc=A, slots=A, pos=A, f=A, T=2, H=2, H_kv=1, d=64, rot=64,
             st=(128, 64, 64, 64, 64, 64, 128, 64), kp=1024, vp=1024, page=16, pages=4, mag=1.0, opt=0, dtype=0):
     return lib.fa_paged_append(q, k, A, qo, kc, A, slots, pos, f, T, H, H_kv, d, rot, L8(*st), kp, vp, page, pages,
