@@ -18,6 +18,7 @@ import datetime
 import hashlib
 import json
 import os
+import re
 import statistics
 import sys
 import threading
@@ -105,16 +106,21 @@ def select_peak(peaks: dict, clocks: dict) -> tuple[float, str]:
                        f"below its maximum {smax:.0f} MHz")
 
 
-def csrc_hash() -> str:
-    """Hash of the sources that the kernels of the traffic table are built from (the rotary and
-    paged-cache files are not among them: fa_lib.cu includes them behind fa_api.cu)."""
-    h = hashlib.sha256()
-    d = os.path.join(ROOT, "exact_io_aware_98_b200", "csrc")
-    for name in sorted(os.listdir(d)):
-        if name.startswith(("fa_paged", "fa_rope", "fa_lib")):
+def csrc_hash(csrc: str = os.path.join(ROOT, "exact_io_aware_98_b200", "csrc")) -> str:
+    """Hash of the sources that the kernels of the traffic table are built from: fa_api.cu and what it
+    includes, directly or not (fa_lib.cu adds the rotary and paged-cache kernels behind it)."""
+    texts, todo = {}, ["fa_api.cu"]
+    while todo:
+        name = todo.pop()
+        path = os.path.join(csrc, name)
+        if name in texts or not os.path.exists(path):  # fa.h is the interface, not a kernel's source
             continue
-        with open(os.path.join(d, name), "rb") as f:
-            h.update(name.encode() + f.read())
+        with open(path, "rb") as f:
+            texts[name] = f.read()
+        todo += [m.decode() for m in re.findall(rb'^\s*#\s*include\s+"([^"]+)"', texts[name], re.M)]
+    h = hashlib.sha256()
+    for name in sorted(texts):
+        h.update(name.encode() + texts[name])
     return h.hexdigest()[:16]
 
 

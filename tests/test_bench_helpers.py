@@ -26,3 +26,17 @@ def test_exp_roof_arithmetic():
     assert r["exp_per_s"] == pytest.approx(1.184e12, rel=1e-3)
     assert r["frac"] == pytest.approx(0.5, abs=1e-4)
     assert bench.exp_roof(1e9, 1.0, None)["sm_mhz"] == 1965.0
+
+
+def test_source_hash_follows_the_includes(tmp_path):
+    """A header counts if the kernels of the traffic table include it, whatever its name."""
+    write = lambda name, text: (tmp_path / name).write_text(text)
+    write("fa_api.cu", '#include "fa.h"\n#include "a.cuh"\n')
+    write("a.cuh", '#pragma once\n#include "fa_paged_shared.cuh"\n#include "a.cuh"\n')
+    write("fa_paged_shared.cuh", "// shared\n")
+    write("fa_paged_own.cuh", "// not included\n")
+    one = bench.csrc_hash(str(tmp_path))
+    write("fa_paged_own.cuh", "// changed\n")
+    assert bench.csrc_hash(str(tmp_path)) == one
+    write("fa_paged_shared.cuh", "// changed\n")
+    assert bench.csrc_hash(str(tmp_path)) != one
