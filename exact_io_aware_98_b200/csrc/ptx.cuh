@@ -11,7 +11,7 @@ namespace fa {
 // ----------------------------------------------------------------------------- status word
 // Device-side status: 0 = OK; otherwise (site << 16) | (blockIdx.x & 0xffff) of the first
 // wait that gave up.  Read and cleared by the host entry point fa_device_status().  Defined
-// here because the library is built as a single translation unit (fa_api.cu).
+// here because the library is built as a single translation unit (fa_lib.cu).
 __device__ unsigned int g_status = 0;
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per wait
