@@ -110,8 +110,10 @@ __device__ __forceinline__ int paged_tiles(int causal, const PagedReq& r, int tp
   return (max(keys, 1) + KT - 1) / KT;
 }
 
-// sum of (a j + b) / m (rounded down) over j in [0, n), a, b >= 0: the Euclidean recursion, two
-// rounds where a divides m or m divides a.  a n + b fits 32 bits.
+// sum of (a j + b) / m (rounded down) over j in [0, n), a, b >= 0: the lattice points under a line, by
+// the Euclidean recursion of floor sums (Graham, Knuth, Patashnik, Concrete Mathematics, section
+// 3.5): take the whole parts of a / m and b / m out, then swap the axes.  Two rounds where a divides m
+// or m divides a.  a n + b fits 32 bits.
 __device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   long long s = 0;
   while (n > 0) {

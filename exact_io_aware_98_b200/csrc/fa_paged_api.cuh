@@ -49,7 +49,16 @@ int rope_vec(int es, int d, int rot, bool rows16) {
 
 // Lays blocks over the work.  A thread walks over several heads where that still leaves every SM
 // enough blocks; otherwise one head per thread, and so few tokens per block that the table of cos
-// and sin is one entry per thread.
+// and sin is one entry per thread.  Measured (back to back in a graph, us) with 8 / 4 / 2 heads per
+// thread and, at the least sizes, the small table; * the rule's choice:
+//   rotation 16 x 16384 x 128             23.7* 27.5  42.7         1024 blocks of 8 heads
+//   rotation 8 x 12 x 1024 x 64           10.6   7.6* 10.7          256
+//   append 8201 tokens, 24 heads, d 64    11.1  11.7* 14.9          387
+//   append 2048 tokens, 48 heads, d 128    9.7  13.4* 20.2          384
+//   append  512 tokens, 48 heads, d 128    5.9   5.7   6.6   7.5*    96
+//   append   64 tokens, 48 heads, d 128    5.7   4.6   4.1   2.9*    12
+// So the two borders (6 blocks of 8 heads per SM, 3/2 of 4) lie on the safe side of the largest and the
+// smallest sizes; between them, where blocks of 8 heads make one or two waves, up to a quarter is lost.
 fa::RopeShape rope_shape(long long N, int heads, int B, int units, int pass, int half) {
   fa::RopeShape sh;
   sh.pass = pass;

@@ -15,8 +15,10 @@
 //   * Rows of the last page behind the last key may hold anything, and 0 * NaN is not 0: the
 //     softmax warpgroups clear those V rows in shared memory before they hand over P.
 // Key tiles: 128 keys at d = 128 (one CTA per SM), 64 at d = 64 (two CTAs per SM), as the forward.
-// Measured: 2048 tokens over 32768 keys, 16 heads over 4: 440 us at d = 128 (1210 TFLOP/s), 391 at
-// d = 64 (680); 8192 tokens of a causal prompt, d = 128: 265-280 us, where the dense forward of the
+// P is rounded to bf16 for P V, the type that the MMA takes beside a bf16 V (its row sum is taken
+// before, in fp32); scores, statistics and sums are fp32.
+// Measured: 2048 tokens over 32768 keys, 16 heads over 4: 440 us at d = 128 (1210 TFLOP/s; 470 to 530
+// where the power limit holds the clock down), 392 at d = 64 (680); 8192 tokens of a causal prompt, d = 128: 265-280 us, where the dense forward of the
 // same box takes 242-258.  The d = 64 tile is bound by the exponentials (62 % of the MUFU's issue
 // slots) and their chain, as there; page sizes 16 to 256 measure alike.
 #pragma once

@@ -13,7 +13,7 @@
 // An SM has about 22 bytes of HBM per cycle, a 64-key tile (d = 128) takes 1490 cycles to arrive,
 // and a group needs about 500 for it, so the stream, not the arithmetic, sets the pace.
 // Measured: 64 requests of up to 16384 keys, 32 heads over 8, d = 128 (2.17 GB): 335 us, 6.5 TB/s,
-// the rate of a copy; 16 requests of 8192 keys: 91 us, 5.9 TB/s (d = 128), 51 us, 5.2 TB/s (d = 64);
+// the rate of a copy; 16 requests of 8192 keys: 96 us, 5.6 TB/s (d = 128), 52 us, 5.2 TB/s (d = 64);
 // one request of 2000 keys: 10 us with its join.
 //
 // Page ids are fetched 8 to 32 tiles ahead.  A page that the table does not name, or that lies behind

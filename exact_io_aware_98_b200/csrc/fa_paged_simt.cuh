@@ -8,12 +8,14 @@
 // one column over all banks.
 //   fa_paged_f32_few_kernel (8 rows, 128 keys a tile, 8 warps): few rows per K/V head (decoding).
 //     Warps in 2 row groups x 4 key groups, 4 rows and 32 keys each; lane = key for the scores, for
-//     P V a lane has the columns lane, lane + 32, ..  Bound by HBM: 16 requests of 8192 keys, 8
-//     heads over 2, take 102 us (2.6 TB/s) at d 128.
+//     P V a lane has the columns lane, lane + 32, ..  Bound by latency: with one K and one V tile a
+//     copy starts only when the phase that reads its buffer is over, and with fewer than 5 rows the
+//     second row group works on none.  16 requests of 8192 keys, 8 heads over 2, d 128: 100 us, 2.7
+//     TB/s of a copy's 6.5.
 //   fa_paged_f32_chunk_kernel (64 rows, 64 keys a tile, 256 threads): a thread forms 4 rows x 4 keys
 //     of scores and 4 rows x 2 NC columns of O (in pairs: one 8-byte read of V, packed FMAs), so
 //     that a value read from shared memory enters four products.  512 tokens over 8192 keys, 16
-//     heads over 4, d 128: 1.01 ms, 34 TFLOP/s (single columns 16 apart: 1.07 ms; a lane per key
+//     heads over 4, d 128: 1.00 ms, 33 TFLOP/s (single columns 16 apart: 1.07 ms; a lane per key
 //     with Q broadcast, 32 rows a tile: 1.16 ms).  Neither FFMA (35 % of its slots) nor shared
 //     memory (57 %) is full: with one or two blocks per SM, latencies between the phases of a tile
 //     remain; unrolling the score loop or leaving its packed FMA out changed nothing.

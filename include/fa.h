@@ -276,8 +276,13 @@ size_t fa_paged_workspace_size(int T, int B, int H, int H_kv, int d);
  *   Lengths    cu_q is clamped to [0, T] and kv_len to [0, max_pages * page_size].  Rows of o
  *              and lse that no request owns are left as they were.
  *   max_q      the most new tokens of any request, as a hint for the choice of kernel only (every
- *              kernel takes every length); <= 0: the mean.
- *   dtype      FA_BF16: d in {64, 128}; q's and the pages' strides multiples of 8 elements.
+ *              kernel takes every length); <= 0: ceil(T / B), where T counts the padding: a step of
+ *              fixed capacity that mostly decodes should pass 1 (or its usual length).  A captured
+ *              call keeps the kernel that it was captured with.
+ *   dtype      FA_BF16: d in {64, 128}; q's and the pages' strides multiples of 8 elements.  Scores,
+ *              maxima and sums are fp32; the probabilities are rounded to bf16 for P V, as in
+ *              fa_fwd, and O once at the end: two roundings of like size, so that O is about
+ *              sqrt(2) times as far from 64 bits as its own rounding (2-norms).
  *              FA_F32: 1 <= d <= 128; CUDA cores, fp32 throughout.
  *   workspace  device memory of at least fa_paged_workspace_size() bytes, 256-byte aligned, scratch
  *              only.  Calls that may overlap on the GPU need one each.
