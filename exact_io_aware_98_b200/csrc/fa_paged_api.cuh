@@ -271,6 +271,15 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return a != nullptr && b != nullptr && x < y + bn && y < x + an;
 }
 
+// Whether [a, a + an) shares a byte with one of `rows` pieces of n bytes, `stride` >= n bytes apart.
+bool overlap_rows(const void* a, size_t an, const void* b, size_t rows, size_t stride, size_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  if (a == nullptr || b == nullptr || an == 0) return false;
+  if (x < y) return y < x + an;
+  const size_t r = (x - y) / stride, in = (x - y) % stride;  // the row at or before a
+  return r < rows && (in < n || (r + 1 < rows && in + an > stride));
+}
+
 // Copies a packed call's arguments (which need not be aligned) after checking their size.
 template <typename Args>
 int unpack(const Args* packed, Args* a) {
@@ -372,19 +381,24 @@ int fa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, const int32_t*
   {
     // blocks read the inputs while others write: an output must not be an input, nor another output
     const size_t b4 = static_cast<size_t>(B) * 4, t4 = static_cast<size_t>(max_tokens) * 4;
-    const size_t table_bytes = (static_cast<size_t>(B - 1) * (B > 1 ? table_stride : 0) + max_pages) * 4;
+    const size_t row = static_cast<size_t>(max_pages) * 4;
+    const size_t stride = B > 1 ? static_cast<size_t>(table_stride) * 4 : row;
+    auto in_table = [&](const void* t, size_t n) { return overlap_rows(t, n, block_table, B, stride, row); };
     const struct {
       const void* p;
       size_t n;
     } in[4] = {{ctx_len, b4}, {new_len, b4}, {free_pages, static_cast<size_t>(n_free) * 4}, {cursor, 4}},
-      out[6] = {{cu_q, b4 + 4}, {kv_len, b4}, {positions, t4}, {slots, 2 * t4}, {counts, 16}, {block_table, table_bytes}};
-    for (const auto& i : in)
-      for (const auto& o : out)
-        if (i.n > 0 && overlap(i.p, i.n, o.p, o.n))
-          return fail(FA_ERR_INVALID, "an output overlaps an input");
-    for (int i = 0; i < 6; ++i)
-      for (int j = 0; j < i; ++j)
-        if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return fail(FA_ERR_INVALID, "two outputs overlap");
+      out[5] = {{cu_q, b4 + 4}, {kv_len, b4}, {positions, t4}, {slots, 2 * t4}, {counts, 16}};
+    for (const auto& i : in) {
+      bool bad = in_table(i.p, i.n);
+      for (const auto& o : out) bad = bad || (i.n > 0 && overlap(i.p, i.n, o.p, o.n));
+      if (bad) return fail(FA_ERR_INVALID, "an output overlaps an input");
+    }
+    for (int i = 0; i < 5; ++i) {
+      bool bad = in_table(out[i].p, out[i].n);
+      for (int j = 0; j < i; ++j) bad = bad || overlap(out[i].p, out[i].n, out[j].p, out[j].n);
+      if (bad) return fail(FA_ERR_INVALID, "two outputs overlap");
+    }
   }
   fa::PlanParams p;
   p.ctx_len = ctx_len;

@@ -66,6 +66,17 @@ def test_plan_outputs_apart(lib):
                 assert "overlap" in lib.fa_get_last_error().decode()
 
 
+def test_plan_outputs_between_the_tables_rows(lib):
+    """A table that is the left part of a wider buffer leaves the space behind its rows to others."""
+    wide = dict(tab=A + 1024, ts=64, mp=8)  # rows of 32 bytes, 256 apart: A + 1024 and A + 1280
+    for name, n in (("counts", 16), ("kv", 8), ("cu", 12), ("pos", 16), ("ctx", 8), ("free", 16)):
+        for at in (A + 1024 + 32, A + 1024 + 256 - n, A + 1280 + 32, A + 1024 - n):
+            assert _plan(lib, **wide, **{name: at}) != INVALID, (name, at - A)
+        for at in (A + 1024, A + 1024 + 28, A + 1280 - n + 4, A + 1280 + 28, A + 1024 - n + 4):
+            assert _plan(lib, **wide, **{name: at}) == INVALID, (name, at - A)
+            assert "overlap" in lib.fa_get_last_error().decode()
+
+
 def _append(lib, q=A, k=A, qo=A + 4096, kc=A, slots=A, pos=A, f=A, T=2, H=2, H_kv=1, d=64, rot=64,
             st=(128, 64, 64, 64, 64, 64, 128, 64), kp=1024, vp=1024, page=16, pages=4, mag=1.0, opt=0, dtype=0):
     return lib.fa_paged_append(q, k, A, qo, kc, A, slots, pos, f, T, H, H_kv, d, rot, L8(*st), kp, vp, page, pages,
