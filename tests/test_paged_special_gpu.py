@@ -49,7 +49,7 @@ def _check(c, t, o, lse):
             clean_q, clean_k = np.where(np.isnan(qh), 0.0, qh), np.where(np.isnan(k), 0.0, k)
             ro, rl, bo, bl = attend_ref(clean_q, clean_k, v, keep, syn.scale_for(c["d"]), c["dtype"])
             assert np.all(np.abs(go - ro)[live] <= bo[live]), f"{where}: O of finite rows"
-            assert np.all(np.abs(gl - rl)[live] <= bl[live]), f"{where}: lse of finite rows"
+            assert np.all(np.abs(gl[live] - rl[live]) <= bl[live]), f"{where}: lse of finite rows"
         at += nq
 
 
